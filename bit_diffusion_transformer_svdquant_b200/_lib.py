@@ -8,7 +8,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-from ctypes import POINTER, byref, c_char_p, c_int, c_size_t, c_ulonglong, c_void_p
+from ctypes import POINTER, byref, c_char_p, c_float, c_int, c_longlong, c_size_t, c_ulonglong, c_void_p
 
 import torch
 
@@ -44,6 +44,32 @@ class SvdqFp8rAct(ctypes.Structure):
                 ("row_scale", c_void_p), ("row_rscale", c_void_p), ("U", c_void_p)]
 
 
+class SvdqMxWeight(ctypes.Structure):
+    _fields_ = [("N", c_int), ("K", c_int), ("r", c_int), ("swiglu_interleaved", c_int), ("n_tile", c_int),
+                ("N_pad", c_int), ("K_pad", c_int), ("reserved0", c_int), ("codes", c_void_p), ("scales", c_void_p),
+                ("inv_lambda", c_void_p), ("L1s_t", c_void_p), ("L2_t", c_void_p), ("tmap", c_ulonglong * 48)]
+
+
+class SvdqMxAct(ctypes.Structure):
+    _fields_ = [("M", c_int), ("K", c_int), ("r", c_int), ("M_pad", c_int), ("K_pad", c_int), ("reserved0", c_int),
+                ("codes", c_void_p), ("scales", c_void_p), ("U", c_void_p)]
+
+
+class SvdqNorm(ctypes.Structure):
+    _fields_ = [("kind", c_int), ("eps", c_float), ("f32", c_int), ("reserved0", c_int), ("weight", c_void_p),
+                ("bias", c_void_p)]
+
+
+class SvdqBlockNormArgs(ctypes.Structure):
+    _fields_ = [("M", c_int), ("D", c_int), ("samples", c_int), ("rows_per_sample", c_int), ("offsets", c_void_p),
+                ("x", c_void_p), ("ldx", c_longlong), ("x_f32", c_int), ("y_f32", c_int), ("y", c_void_p),
+                ("ldy", c_longlong), ("x_out", c_void_p), ("ld_out", c_longlong), ("h", c_void_p),
+                ("ldh", c_longlong), ("h_f32", c_int), ("mod_f32", c_int), ("gate", c_void_p),
+                ("ld_gate", c_longlong), ("scale", c_void_p), ("ld_scale", c_longlong), ("shift", c_void_p),
+                ("ld_shift", c_longlong), ("skip_scale", c_float), ("res_scale", c_float), ("post", SvdqNorm),
+                ("norm", SvdqNorm)]
+
+
 class SvdqError(RuntimeError):
     def __init__(self, func: str, status: int, message: str):
         super().__init__(f"{func}: {STATUS_NAMES.get(status, status)}: {message}")
@@ -56,6 +82,7 @@ _lib = None
 def _declare(lib):
     W, A = POINTER(SvdqWeight), POINTER(SvdqAct)
     FW, FA = POINTER(SvdqFp8rWeight), POINTER(SvdqFp8rAct)
+    MW, MA, BN = POINTER(SvdqMxWeight), POINTER(SvdqMxAct), POINTER(SvdqBlockNormArgs)
     sig = {
         "svdq_fp8r_weight_bytes": (c_size_t, [c_int, c_int, c_int]),
         "svdq_fp8r_act_bytes": (c_size_t, [c_int, c_int, c_int]),
@@ -66,6 +93,19 @@ def _declare(lib):
         "svdq_fp8r_gemm": (c_int, [FA, FW, c_void_p, c_int, c_void_p, c_int, c_void_p]),
         "svdq_fp8r_export_weight": (c_int, [FW, c_void_p, c_void_p, c_void_p]),
         "svdq_fp8r_export_act": (c_int, [FA, c_void_p, c_void_p, c_void_p]),
+        "svdq_mx_weight_bytes": (c_size_t, [c_int, c_int, c_int, c_int]),
+        "svdq_mx_act_bytes": (c_size_t, [c_int, c_int, c_int]),
+        "svdq_mx_pack_weight": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
+                                        c_void_p, c_size_t, MW, c_void_p]),
+        "svdq_mx_weight_bind": (c_int, [c_int, c_int, c_int, c_int, c_void_p, c_size_t, MW]),
+        "svdq_mx_act_bind": (c_int, [c_int, c_int, c_int, c_void_p, c_size_t, MA]),
+        "svdq_mx_quantize_act": (c_int, [c_void_p, c_longlong, MW, MA, c_void_p]),
+        "svdq_mx_gemm": (c_int, [MA, MW, c_void_p, c_int, c_void_p, c_longlong, c_int, c_void_p]),
+        "svdq_mx_export_weight": (c_int, [MW, c_void_p, c_void_p, c_void_p]),
+        "svdq_mx_export_act": (c_int, [MA, c_void_p, c_void_p, c_void_p]),
+        "svdq_mx_dequantize_act": (c_int, [MA, c_void_p, c_longlong, c_int, c_void_p]),
+        "svdq_block_norm": (c_int, [BN, c_void_p]),
+        "svdq_block_norm_quantize_mx": (c_int, [BN, MW, MA, c_void_p]),
         "svdq_mlp_scratch_bytes": (c_size_t, [c_int, c_int]),
         "svdq_gemm_swiglu_quant": (c_int, [A, W, c_void_p, W, c_void_p, A, c_void_p, c_size_t, c_void_p, c_void_p]),
         "svdq_gemm_swiglu_quant_noscratch": (c_int, [A, W, c_void_p, W, c_void_p, A, c_void_p, c_void_p]),
@@ -444,6 +484,339 @@ def export_act_fp8r(act: Fp8rAct):
         _check("svdq_fp8r_export_act", lib().svdq_fp8r_export_act(byref(act.desc), _ptr(codes), _ptr(scales),
                                                                   _stream(act.device)))
     return codes, scales
+
+
+# ---------------------------------------------------------------- MXFP4 variant
+
+def _rows(t, dtype, name, dim):
+    """A CUDA matrix whose rows are contiguous (any row stride)."""
+    if not t.is_cuda or t.dtype != dtype or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected a two-dimensional CUDA {dtype} tensor with contiguous rows, got "
+                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    if t.shape[1] != dim:
+        raise ValueError(f"{name}: rows of {t.shape[1]}, expected {dim}")
+    return t.stride(0) if t.shape[0] > 1 else max(dim, t.stride(0))
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+class MxWeight:
+    """One layer's weight packed as MXFP4 (E2M1 codes, one E8M0 scale per 32 elements along K) with its
+    16-bit branch. inv_lambda None: no smoothing. N and K need only be multiples of 8."""
+
+    def __init__(self, R: torch.Tensor, L1s: torch.Tensor | None = None, L2: torch.Tensor | None = None,
+                 inv_lambda: torch.Tensor | None = None, swiglu: bool = False):
+        _need(R, torch.float32, "R", 2)
+        N, K = R.shape
+        if inv_lambda is not None:
+            _need(inv_lambda, torch.float32, "inv_lambda", 1)
+            if inv_lambda.shape[0] != K:
+                raise ValueError("inv_lambda must be [K]")
+        r = 0 if L1s is None else L1s.shape[1]
+        if r:
+            _need(L1s, torch.bfloat16, "L1s", 2)
+            _need(L2, torch.bfloat16, "L2", 2)
+            if tuple(L1s.shape) != (K, r) or tuple(L2.shape) != (r, N):
+                raise ValueError("L1s must be [K, r] and L2 [r, N]")
+        _same_device(R.device, L1s=L1s, L2=L2, inv_lambda=inv_lambda)
+        self._allocate(N, K, r, swiglu, R.device)
+        with torch.cuda.device(self.device):
+            _check("svdq_mx_pack_weight", lib().svdq_mx_pack_weight(
+                _ptr(R), _ptr(L1s) if r else None, _ptr(L2) if r else None, _ptr(inv_lambda), N, K, r,
+                1 if swiglu else 0, _ptr(self.buf), self.buf.numel(), byref(self.desc), _stream(self.device)))
+
+    def _allocate(self, N, K, r, swiglu, device):
+        nbytes = lib().svdq_mx_weight_bytes(N, K, r, 1 if swiglu else 0)
+        if nbytes == 0:
+            raise SvdqError("svdq_mx_weight_bytes", 2, f"unsupported shape N={N} K={K} r={r} swiglu={swiglu}")
+        self.buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.device = self.buf.device
+        self.desc = SvdqMxWeight()
+        self.N, self.K, self.r, self.swiglu = N, K, r, bool(swiglu)
+
+    @property
+    def n_tile(self) -> int:
+        return self.desc.n_tile
+
+    def state_dict(self) -> dict:
+        """The packed blob (on the host) and what re-binds it, as PackedWeight.state_dict."""
+        return {"abi": lib().svdq_abi_version(), "format": "mxfp4", "N": self.N, "K": self.K, "r": self.r,
+                "swiglu": self.swiglu, "blob": self.buf.cpu()}
+
+    @classmethod
+    def from_state(cls, state: dict, device) -> "MxWeight":
+        if state["abi"] != lib().svdq_abi_version() or state.get("format") != "mxfp4":
+            raise ValueError(f"checkpoint ABI {state['abi']} format {state.get('format')}: expected ABI "
+                             f"{lib().svdq_abi_version()} format mxfp4")
+        blob = state["blob"]
+        need = lib().svdq_mx_weight_bytes(state["N"], state["K"], state["r"], 1 if state["swiglu"] else 0)
+        if not isinstance(blob, torch.Tensor) or blob.dtype != torch.uint8 or blob.dim() != 1 \
+                or not blob.is_contiguous() or need == 0 or blob.numel() != need:
+            raise ValueError(f"checkpoint blob: expected a contiguous one-dimensional uint8 tensor of {need} bytes")
+        self = cls.__new__(cls)
+        self._allocate(state["N"], state["K"], state["r"], state["swiglu"], device)
+        self.buf.copy_(blob)
+        with torch.cuda.device(self.device):
+            _check("svdq_mx_weight_bind", lib().svdq_mx_weight_bind(
+                self.N, self.K, self.r, 1 if self.swiglu else 0, _ptr(self.buf), self.buf.numel(), byref(self.desc)))
+        return self
+
+
+class MxAct:
+    """An MXFP4 activation buffer for M rows (codes, scales, U)."""
+
+    def __init__(self, M: int, K: int, r: int, device):
+        nbytes = lib().svdq_mx_act_bytes(M, K, r)
+        if nbytes == 0:
+            raise SvdqError("svdq_mx_act_bytes", 2, f"unsupported shape M={M} K={K} r={r}")
+        self.buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.desc = SvdqMxAct()
+        _check("svdq_mx_act_bind", lib().svdq_mx_act_bind(M, K, r, _ptr(self.buf), nbytes, byref(self.desc)))
+        self.M, self.K, self.r, self.device = M, K, r, self.buf.device
+
+    def U(self) -> torch.Tensor:
+        """[2, M_pad, r] bf16: the hi and lo halves of X L1s."""
+        n, off = self.desc.M_pad * self.r, self.desc.U - self.buf.data_ptr()
+        return self.buf[off:off + 4 * n].view(torch.bfloat16).view(2, self.desc.M_pad, self.r)
+
+
+def quantize_act_mx(X: torch.Tensor, w: MxWeight, act: MxAct) -> MxAct:
+    """Smoothing + MXFP4 quantization + low-rank down-projection in one pass over X [M, K] (rows of
+    any 16-byte stride)."""
+    ldx = _rows(X, torch.bfloat16, "X", w.K)
+    if X.shape[0] != act.M:
+        raise ValueError("X shape does not match the act buffer / weight")
+    _same_device(X.device, weight=w, act=act)
+    with torch.cuda.device(X.device):
+        _check("svdq_mx_quantize_act", lib().svdq_mx_quantize_act(_ptr(X), ldx, byref(w.desc), byref(act.desc),
+                                                                  _stream(X.device)))
+    return act
+
+
+def gemm_mx(act: MxAct, w: MxWeight, bias: torch.Tensor | None = None, epilogue: int | None = None,
+            out_dtype=torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The MXFP4 GEMM + low-rank up-projection + bias / SwiGLU epilogue. `out` may have any row stride
+    of whole 16-byte units."""
+    if epilogue is None:
+        epilogue = (EPI_BIAS if bias is not None else EPI_NONE) | (EPI_SWIGLU if w.swiglu else 0)
+    n_out = w.N // 2 if epilogue & EPI_SWIGLU else w.N
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"out_dtype {out_dtype}: expected bfloat16 or float32")
+    if out is None:
+        out = torch.empty(act.M, n_out, dtype=out_dtype, device=act.device)
+    ldy = _rows(out, out_dtype, "out", n_out)
+    if out.shape[0] != act.M:
+        raise ValueError(f"out: {out.shape[0]} rows, expected {act.M}")
+    if bias is not None:
+        _need(bias, torch.bfloat16, "bias", 1)
+        if bias.shape[0] != w.N:
+            raise ValueError("bias must be [N]")
+    _same_device(act.device, weight=w, bias=bias, out=out)
+    code = OUT_F32 if out_dtype == torch.float32 else OUT_BF16
+    with torch.cuda.device(act.device):
+        _check("svdq_mx_gemm", lib().svdq_mx_gemm(byref(act.desc), byref(w.desc), _ptr(bias), epilogue, _ptr(out),
+                                                  ldy, code, _stream(act.device)))
+    return out
+
+
+def linear_mx(X, w: MxWeight, bias=None, act: MxAct | None = None, out=None, out_dtype=torch.bfloat16):
+    """The whole MXFP4 layer on the current stream (the format has no tensor scale to calibrate)."""
+    act = MxAct(X.shape[0], w.K, w.r, X.device) if act is None else act
+    quantize_act_mx(X, w, act)
+    return gemm_mx(act, w, bias, out=out, out_dtype=out_dtype)
+
+
+def _export_mx(fn, obj, rows):
+    codes = torch.empty(rows, obj.K // 2, dtype=torch.uint8, device=obj.device)
+    scales = torch.empty(rows, (obj.K + 31) // 32, dtype=torch.uint8, device=obj.device)
+    with torch.cuda.device(obj.device):
+        _check(fn, getattr(lib(), fn)(byref(obj.desc), _ptr(codes), _ptr(scales), _stream(obj.device)))
+    return codes, scales
+
+
+def export_weight_mx(w: MxWeight):
+    return _export_mx("svdq_mx_export_weight", w, w.N)
+
+
+def export_act_mx(act: MxAct):
+    return _export_mx("svdq_mx_export_act", act, act.M)
+
+
+def dequantize_act_mx(act: MxAct, out: torch.Tensor | None = None, out_dtype=torch.bfloat16) -> torch.Tensor:
+    """The values the quantized (smoothed) activation stands for, [M, K]."""
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"out_dtype {out_dtype}: expected bfloat16 or float32")
+    if out is None:
+        out = torch.empty(act.M, act.K, dtype=out_dtype, device=act.device)
+    ld = _rows(out, out_dtype, "out", act.K)
+    if out.shape[0] != act.M:
+        raise ValueError(f"out: {out.shape[0]} rows, expected {act.M}")
+    _same_device(act.device, out=out)
+    code = OUT_F32 if out_dtype == torch.float32 else OUT_BF16
+    with torch.cuda.device(act.device):
+        _check("svdq_mx_dequantize_act", lib().svdq_mx_dequantize_act(byref(act.desc), _ptr(out), ld, code,
+                                                                      _stream(act.device)))
+    return out
+
+
+# ---------------------------------------------------------------- block norms
+
+NORM_KINDS = {"rms": 1, "layer": 2}
+
+
+class Norm:
+    """One normalisation of rows of D: "rms" (v / sqrt(mean(v^2) + eps)) or "layer" (mean removed), times
+    weight, plus bias (each optional, [D], bf16 or fp32, both of one type)."""
+
+    def __init__(self, kind: str, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                 eps: float = 1e-6):
+        if kind not in NORM_KINDS:
+            raise ValueError(f"norm kind {kind!r}: expected one of {sorted(NORM_KINDS)}")
+        if not eps >= 0.0:
+            raise ValueError(f"eps {eps}: expected a non-negative number")
+        self.kind, self.eps, self.weight, self.bias = kind, float(eps), weight, bias
+        self.D = self.device = None
+        given = [v for v in (weight, bias) if v is not None]
+        for v in given:
+            if v.dtype not in (torch.bfloat16, torch.float32) or not v.is_cuda or v.dim() != 1 \
+                    or not v.is_contiguous() or v.dtype != given[0].dtype or v.shape != given[0].shape:
+                raise ValueError("weight and bias: expected contiguous CUDA [D] tensors of one type, bf16 or fp32")
+        self.desc = SvdqNorm(kind=NORM_KINDS[kind], eps=self.eps)
+        if given:
+            self.D, self.device = given[0].shape[0], given[0].device
+            self.desc.f32 = given[0].dtype == torch.float32
+            self.desc.weight, self.desc.bias = _ptr(weight), _ptr(bias)
+            _same_device(self.device, weight=weight, bias=bias)
+
+
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+def _norm_rows(t, name, shape=None, device=None):
+    """(pointer, row stride, fp32 flag) of a [M, D] or [B, T, D] activation whose rows are evenly spaced."""
+    if t.dtype not in _FLOATS or not t.is_cuda or t.dim() not in (2, 3):
+        raise ValueError(f"{name}: expected a CUDA bf16 or fp32 tensor [rows, D] or [samples, rows, D], got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    st, sh = t.stride(), t.shape
+    D, T = sh[-1], sh[-2]
+    ld = st[-2] if T > 1 else (st[0] if len(sh) == 3 and sh[0] > 1 else D)
+    if (D > 1 and st[-1] != 1) or (len(sh) == 3 and sh[0] > 1 and T > 1 and st[0] != T * ld):
+        raise ValueError(f"{name}: rows must be contiguous and evenly spaced, got strides {st}")
+    if ld < D and t.numel() and t.shape[:-1].numel() > 1:
+        raise ValueError(f"{name}: rows overlap (strides {st})")
+    return t.data_ptr(), max(ld, D), t.dtype == torch.float32
+
+
+def _norm_args(x, y, gate, post, res_scale, skip_scale, norm, scale, shift, offsets, out, h):
+    a = SvdqBlockNormArgs()
+    device, shape = x.device, x.shape
+    a.x, a.ldx, a.x_f32 = _norm_rows(x, "x")
+    D = shape[-1]
+    a.M, a.D = shape[:-1].numel(), D
+    if offsets is not None:
+        if len(shape) != 2:
+            raise ValueError("x: expected [rows, D] with offsets")
+        if offsets.dtype != torch.int32 or offsets.device != device or offsets.dim() != 1 or offsets.shape[0] < 2 \
+                or not offsets.is_contiguous():
+            raise ValueError("offsets: expected a contiguous int32 [samples + 1] tensor on x's device")
+        a.samples, a.offsets = offsets.shape[0] - 1, offsets.data_ptr()
+    else:
+        a.samples, a.rows_per_sample = (shape[0], max(1, shape[1])) if len(shape) == 3 else (1, max(1, shape[0]))
+        a.samples = max(1, a.samples)
+    mods = [m for m in (gate, scale, shift) if m is not None]
+    if mods:
+        a.mod_f32 = mods[0].dtype == torch.float32
+    for name, m in (("gate", gate), ("scale", scale), ("shift", shift)):
+        if m is None:
+            continue
+        if m.dtype not in _FLOATS or m.dtype != mods[0].dtype or m.device != device:
+            raise ValueError("gate, scale and shift: expected tensors of one type, bf16 or fp32, on x's device")
+        if m.shape not in ((D,), (1, D), (a.samples, D)) or (D > 1 and m.stride(-1) != 1):
+            raise ValueError(f"{name}: shape {tuple(m.shape)}, expected [D] or [samples, D] = [{a.samples}, {D}] with "
+                             "contiguous rows")
+        setattr(a, name, m.data_ptr())
+        setattr(a, "ld_" + name, m.stride(0) if m.dim() == 2 and m.shape[0] > 1 else 0)
+    for name, n in (("post", post), ("norm", norm)):
+        if n is not None:
+            if n.D is not None and (n.D != D or n.device != device):
+                raise ValueError(f"{name}: vectors of {n.D} on {n.device}, expected {D} on {device}")
+            setattr(a, name, n.desc)
+    if y is not None:
+        a.y, a.ldy, a.y_f32 = _norm_rows(y, "y", shape, device)
+        if out is not None:
+            a.x_out, a.ld_out, f32 = _norm_rows(out, "out", shape, device)
+            if f32 != a.x_f32:
+                raise ValueError(f"out: {out.dtype}, expected x's {x.dtype}")
+        a.skip_scale, a.res_scale = skip_scale, res_scale
+    if h is not None:
+        a.h, a.ldh, a.h_f32 = _norm_rows(h, "h", shape, device)
+    return a
+
+
+def _run_norm(a, device, w=None, act=None):
+    if a.M == 0:
+        return  # no row: empty tensors have no address to pass
+    with torch.cuda.device(device):
+        if act is None:
+            _check("svdq_block_norm", lib().svdq_block_norm(byref(a), _stream(device)))
+        else:
+            _same_device(device, weight=w, act=act)
+            _check("svdq_block_norm_quantize_mx", lib().svdq_block_norm_quantize_mx(
+                byref(a), byref(w.desc), byref(act.desc), _stream(device)))
+
+
+def block_norm(x, norm: Norm, scale=None, shift=None, offsets=None, out=None, out_dtype=None):
+    """h = norm(x) (1 + scale) + shift over the last axis of x [rows, D] or [samples, rows, D]; scale and
+    shift [D] or one row per sample. `offsets` (int32 [samples + 1]) gives packed samples of x [rows, D];
+    rows outside them are left as they are in `out`. out_dtype defaults to x's (or out's) type."""
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out: {out.dtype}, expected {out_dtype}")
+    _run_norm(_norm_args(x, None, None, None, 1.0, 1.0, norm, scale, shift, offsets, None, out), x.device)
+    return out
+
+
+def gated_residual(x, y, gate=None, post: Norm | None = None, res_scale: float = 1.0, skip_scale: float = 1.0,
+                   norm: Norm | None = None, scale=None, shift=None, offsets=None, out=None, h=None, h_dtype=None):
+    """A block's end, x' = skip_scale x + res_scale gate post(y), and (with `norm`) the next block's
+    norm h = norm(x') (1 + scale) + shift, in one pass. Returns x', or (x', h). `out` may be x itself
+    (the residual stream updated in place). h_dtype defaults to y's type."""
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    if norm is None and (h is not None or h_dtype is not None):
+        raise ValueError("h without a norm")
+    if norm is not None and h is None:
+        h = torch.empty(x.shape, dtype=h_dtype or y.dtype, device=x.device)
+    elif h is not None and h_dtype is not None and h.dtype != h_dtype:
+        raise ValueError(f"h: {h.dtype}, expected {h_dtype}")
+    _run_norm(_norm_args(x, y, gate, post, res_scale, skip_scale, norm, scale, shift, offsets, out, h), x.device)
+    return out if norm is None else (out, h)
+
+
+def norm_quantize_act_mx(x, norm: Norm, w: MxWeight, act: MxAct, scale=None, shift=None, offsets=None) -> MxAct:
+    """block_norm whose bf16 result is quantized for the next layer instead of stored: the codes and
+    scales quantize_act_mx makes of it. For weights without a branch."""
+    _run_norm(_norm_args(x, None, None, None, 1.0, 1.0, norm, scale, shift, offsets, None, None), x.device, w, act)
+    return act
+
+
+def gated_residual_quantize_mx(x, y, norm: Norm, w: MxWeight, act: MxAct, gate=None, post: Norm | None = None,
+                               res_scale: float = 1.0, skip_scale: float = 1.0, scale=None, shift=None, offsets=None,
+                               out=None):
+    """gated_residual with norm whose bf16 h is quantized for the next layer instead of stored. Returns
+    (x', act). For weights without a branch."""
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    _run_norm(_norm_args(x, y, gate, post, res_scale, skip_scale, norm, scale, shift, offsets, out, None), x.device, w,
+              act)
+    return out, act
 
 
 def device_status(reset: bool = True) -> int:

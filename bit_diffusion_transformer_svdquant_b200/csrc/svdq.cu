@@ -16,6 +16,8 @@
 #include "svdq_fp8r.cuh"
 #include "svdq_fused.cuh"
 #include "svdq_gemm.cuh"
+#include "svdq_mx.cuh"
+#include "svdq_norm.cuh"
 #include "svdq_ptx.cuh"
 #include "svdq_quant.cuh"
 
@@ -1430,6 +1432,657 @@ svdq_status svdq_gemm_swiglu_quant_noscratch(const svdq_act* act, const svdq_wei
   if (svdq_status s = builtin_scratch_ptr(&scratch); s != SVDQ_OK) return s;
   return svdq_gemm_swiglu_quant(act, w, bias, w_next, g_x_next, act_next, scratch, kMlpBuiltinScratchBytes, H,
                                 stream);
+}
+
+}  // extern "C"
+
+
+// ================================================================== MXFP4 variant
+namespace {
+
+constexpr int kMxStages384 = 4;
+constexpr int kMxStages256 = 5;
+constexpr int kMxStages128 = 7;
+template <int N_TILE, int STAGES>
+using MxLayout = svdq::PairGemmLayout<true, N_TILE, STAGES, svdq::mx::Gemm::kSfAtomsK>;
+
+struct MxState {
+  bool ready = false;
+  int max_pairs[3] = {0, 0, 0};  // co-resident CTA pairs of the MXFP4 GEMM for n_tile 384, 256, 128
+};
+MxState g_mx[64];
+
+template <int N_TILE, int STAGES>
+svdq_status mx_gemm_setup(int sms, int* max_pairs) {
+  auto* kern = svdq::pair_gemm_kernel<svdq::mx::Gemm, N_TILE, STAGES>;
+  SVDQ_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MxLayout<N_TILE, STAGES>::kSmem));
+  return fp8r_max_pairs(reinterpret_cast<const void*>(kern), MxLayout<N_TILE, STAGES>::kSmem, sms, max_pairs);
+}
+template <int R>
+svdq_status mx_quant_setup() {
+  auto* kern = svdq::quant_act_kernel<R, svdq::mx::Act>;
+  SVDQ_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, svdq::Q1Layout<R>::kSmem));
+  return SVDQ_OK;
+}
+
+// The MXFP4 kernels are set up on the first MXFP4 call on a device.
+svdq_status mx_ready(int* dev_out, int* sm_out) {
+  int dev = 0, sms = 0;
+  if (svdq_status s = device_ready(&dev, &sms); s != SVDQ_OK) return s;
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  MxState& st = g_mx[dev];
+  if (!st.ready) {
+    svdq_status s = mx_gemm_setup<384, kMxStages384>(sms, &st.max_pairs[0]);
+    if (s == SVDQ_OK) s = mx_gemm_setup<256, kMxStages256>(sms, &st.max_pairs[1]);
+    if (s == SVDQ_OK) s = mx_gemm_setup<128, kMxStages128>(sms, &st.max_pairs[2]);
+    if (s == SVDQ_OK) s = mx_quant_setup<0>();
+    if (s == SVDQ_OK) s = mx_quant_setup<16>();
+    if (s == SVDQ_OK) s = mx_quant_setup<32>();
+    if (s == SVDQ_OK) s = mx_quant_setup<64>();
+    if (s != SVDQ_OK) return s;
+    st.ready = true;
+  }
+  if (dev_out) *dev_out = dev;
+  if (sm_out) *sm_out = sms;
+  return SVDQ_OK;
+}
+
+constexpr int kMxMax = 1 << 20;
+bool mx_k_ok(int K) { return K > 0 && K % 8 == 0 && K <= kMxMax; }
+bool mx_n_ok(int N, int swiglu) { return N > 0 && N % (swiglu ? 16 : 8) == 0 && N <= kMxMax; }
+int mx_k_pad(int K) { return (K + 255) / 256 * 256; }
+int round_up(int x, int to) { return (x + to - 1) / to * to; }
+
+// GEMM tile width along N: the widest whose padding adds no 128-column block; SwiGLU pairs gate and up
+// columns inside a tile of 256.
+int mx_n_tile(int N, int swiglu) {
+  if (swiglu) return 256;
+  const int least = round_up(N, 128);
+  if (least % 384 == 0) return 384;
+  return least % 256 == 0 ? 256 : 128;
+}
+int mx_n_pad(int N, int swiglu) {
+  return swiglu ? round_up(N / 2, 128) * 2 : round_up(N, mx_n_tile(N, 0));
+}
+
+struct MxWeightLayout {
+  size_t codes, scales, inv_lambda, l1t, l2t, total;
+};
+MxWeightLayout mx_weight_layout(int N_pad, int K_pad, int r) {
+  MxWeightLayout l{};
+  size_t off = 0;
+  l.codes = off;
+  off = align_up(off + static_cast<size_t>(N_pad) * K_pad / 2);
+  l.scales = off;
+  off = align_up(off + static_cast<size_t>(N_pad) * (K_pad / 32));
+  l.inv_lambda = off;
+  off = align_up(off + static_cast<size_t>(K_pad) * 4);
+  l.l1t = off;
+  off = align_up(off + static_cast<size_t>(r) * K_pad * 2);
+  l.l2t = off;
+  off = align_up(off + static_cast<size_t>(N_pad) * r * 2);
+  l.total = off;
+  return l;
+}
+
+struct MxActLayout {
+  size_t codes, scales, u, total;
+  int M_pad, K_pad;
+};
+MxActLayout mx_act_layout(int M, int K, int r) {
+  MxActLayout l{};
+  l.M_pad = round_up(M, 128);
+  l.K_pad = mx_k_pad(K);
+  size_t off = 0;
+  l.codes = off;
+  off = align_up(off + static_cast<size_t>(l.M_pad) * l.K_pad / 2);
+  l.scales = off;
+  off = align_up(off + static_cast<size_t>(l.M_pad) * (l.K_pad / 32));
+  l.u = off;
+  off = align_up(off + static_cast<size_t>(l.M_pad) * r * 2 * 2);  // hi and lo halves
+  l.total = off;
+  return l;
+}
+
+svdq_status check_mx_weight(const svdq_mx_weight* w) {
+  const int sw = w->swiglu_interleaved;
+  if ((sw != 0 && sw != 1) || !mx_n_ok(w->N, sw) || !mx_k_ok(w->K) || !valid_r(w->r) || w->n_tile != mx_n_tile(w->N, sw) ||
+      w->N_pad != mx_n_pad(w->N, sw) || w->K_pad != mx_k_pad(w->K))
+    return fail(SVDQ_ERR_INVALID_ARG,
+                "MXFP4 weight descriptor N=%d K=%d r=%d n_tile=%d is not one svdq_mx_pack_weight makes", w->N, w->K,
+                w->r, w->n_tile);
+  if (w->codes == nullptr || w->scales == nullptr || w->inv_lambda == nullptr ||
+      (w->r > 0 && (w->L1s_t == nullptr || w->L2_t == nullptr)))
+    return fail(SVDQ_ERR_INVALID_ARG, "MXFP4 weight descriptor has a null buffer");
+  return SVDQ_OK;
+}
+
+svdq_status check_mx_act(const svdq_mx_act* a) {
+  if (a->M < 1 || a->M >= (1 << 24) || !mx_k_ok(a->K) || !valid_r(a->r) || a->M_pad != round_up(a->M, 128) ||
+      a->K_pad != mx_k_pad(a->K))
+    return fail(SVDQ_ERR_INVALID_ARG, "MXFP4 act descriptor M=%d M_pad=%d K=%d r=%d is not one svdq_mx_act_bind makes",
+                a->M, a->M_pad, a->K, a->r);
+  if (a->codes == nullptr || a->scales == nullptr || (a->r > 0 && a->U == nullptr))
+    return fail(SVDQ_ERR_INVALID_ARG, "MXFP4 act descriptor has a null buffer");
+  return SVDQ_OK;
+}
+
+svdq_status mx_fill_weight(uint8_t* b, int N, int K, int r, int swiglu, svdq_mx_weight* out) {
+  svdq_mx_weight w{};
+  w.N = N;
+  w.K = K;
+  w.r = r;
+  w.swiglu_interleaved = swiglu ? 1 : 0;
+  w.n_tile = mx_n_tile(N, swiglu);
+  w.N_pad = mx_n_pad(N, swiglu);
+  w.K_pad = mx_k_pad(K);
+  const MxWeightLayout l = mx_weight_layout(w.N_pad, w.K_pad, r);
+  w.codes = b + l.codes;
+  w.scales = b + l.scales;
+  w.inv_lambda = reinterpret_cast<float*>(b + l.inv_lambda);
+  w.L1s_t = b + l.l1t;
+  w.L2_t = b + l.l2t;
+  static_assert(sizeof(w.tmap) >= 3 * sizeof(CUtensorMap), "tmap storage");
+  CUtensorMap tmB, tmL2, tmL1;
+  std::memset(&tmL2, 0, sizeof(tmL2));
+  std::memset(&tmL1, 0, sizeof(tmL1));
+  if (svdq_status s = make_tmap(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, w.K_pad / 2, w.N_pad, w.K_pad / 2, 128,
+                                w.n_tile / 2, CU_TENSOR_MAP_SWIZZLE_128B);
+      s != SVDQ_OK)
+    return s;
+  if (r > 0) {
+    if (svdq_status s = make_tmap(&tmL2, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, w.L2_t, r, w.N_pad,
+                                  static_cast<uint64_t>(r) * 2, r < 32 ? r : 32, w.n_tile / 2, lr_swizzle(r));
+        s != SVDQ_OK)
+      return s;
+    if (svdq_status s = make_tmap(&tmL1, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, w.L1s_t, w.K_pad, r,
+                                  static_cast<uint64_t>(w.K_pad) * 2, 64, r, CU_TENSOR_MAP_SWIZZLE_128B);
+        s != SVDQ_OK)
+      return s;
+  }
+  std::memcpy(&w.tmap[0][0], &tmB, sizeof(CUtensorMap));
+  std::memcpy(&w.tmap[1][0], &tmL2, sizeof(CUtensorMap));
+  std::memcpy(&w.tmap[2][0], &tmL1, sizeof(CUtensorMap));
+  *out = w;
+  return SVDQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t svdq_mx_weight_bytes(int N, int K, int r, int swiglu) {
+  if (!mx_n_ok(N, swiglu) || !mx_k_ok(K) || !valid_r(r)) return 0;
+  return mx_weight_layout(mx_n_pad(N, swiglu), mx_k_pad(K), r).total;
+}
+
+size_t svdq_mx_act_bytes(int M, int K, int r) {
+  if (M < 1 || M >= (1 << 24) || !mx_k_ok(K) || !valid_r(r)) return 0;
+  return mx_act_layout(M, K, r).total;
+}
+
+svdq_status svdq_mx_act_bind(int M, int K, int r, void* dst, size_t dst_bytes, svdq_mx_act* out) {
+  if (out == nullptr || dst == nullptr) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
+  const size_t need = svdq_mx_act_bytes(M, K, r);
+  if (need == 0) return fail(SVDQ_ERR_UNSUPPORTED, "MXFP4 act shape M=%d K=%d r=%d unsupported", M, K, r);
+  if (dst_bytes < need) return fail(SVDQ_ERR_INVALID_ARG, "MXFP4 act buffer %zu bytes < %zu", dst_bytes, need);
+  if (reinterpret_cast<uintptr_t>(dst) % kAlign) return fail(SVDQ_ERR_UNSUPPORTED, "act buffer not 256-byte aligned");
+  const MxActLayout l = mx_act_layout(M, K, r);
+  uint8_t* b = static_cast<uint8_t*>(dst);
+  svdq_mx_act a{};
+  a.M = M;
+  a.K = K;
+  a.r = r;
+  a.M_pad = l.M_pad;
+  a.K_pad = l.K_pad;
+  a.codes = b + l.codes;
+  a.scales = b + l.scales;
+  a.U = b + l.u;
+  *out = a;
+  return SVDQ_OK;
+}
+
+svdq_status svdq_mx_pack_weight(const float* R_nk, const uint16_t* L1s_kr, const uint16_t* L2_rn,
+                                const float* inv_lambda, int N, int K, int r, int swiglu, void* dst, size_t dst_bytes,
+                                svdq_mx_weight* out, svdq_stream_t stream) {
+  if (out == nullptr || R_nk == nullptr || dst == nullptr) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
+  if (r > 0 && (L1s_kr == nullptr || L2_rn == nullptr)) return fail(SVDQ_ERR_INVALID_ARG, "null L1s / L2 with r > 0");
+  const size_t need = svdq_mx_weight_bytes(N, K, r, swiglu);
+  if (need == 0) return fail(SVDQ_ERR_UNSUPPORTED, "MXFP4 weight shape N=%d K=%d r=%d unsupported", N, K, r);
+  if (!aligned16(R_nk) || (r > 0 && (!aligned16(L1s_kr) || !aligned16(L2_rn))) ||
+      (reinterpret_cast<uintptr_t>(inv_lambda) & 3u))
+    return fail(SVDQ_ERR_UNSUPPORTED, "inputs must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(dst) % kAlign) return fail(SVDQ_ERR_UNSUPPORTED, "dst not 256-byte aligned");
+  if (dst_bytes < need) return fail(SVDQ_ERR_INVALID_ARG, "MXFP4 weight buffer %zu bytes < %zu", dst_bytes, need);
+  int dev, sms;
+  if (svdq_status s = mx_ready(&dev, &sms); s != SVDQ_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  svdq_mx_weight w{};
+  if (svdq_status s = mx_fill_weight(static_cast<uint8_t*>(dst), N, K, r, swiglu, &w); s != SVDQ_OK) return s;
+  SVDQ_CUDA(cudaMemsetAsync(dst, 0, need, st));  // padded rows and columns
+  svdq::mx::fill_inv_lambda_kernel<<<grid_for(w.K_pad, 256, sms), 256, 0, st>>>(inv_lambda, K, w.K_pad, w.inv_lambda);
+  if (svdq_status s = check_launch("mx::fill_inv_lambda_kernel"); s != SVDQ_OK) return s;
+  svdq::mx::pack_quant_kernel<<<grid_for(static_cast<size_t>(N) * w.K_pad / 8, 256, sms), 256, 0, st>>>(
+      R_nk, N, K, w.K_pad, w.n_tile, w.swiglu_interleaved, static_cast<uint8_t*>(w.codes),
+      static_cast<uint8_t*>(w.scales));
+  if (svdq_status s = check_launch("mx::pack_quant_kernel"); s != SVDQ_OK) return s;
+  if (r > 0) {
+    svdq::mx::transpose_l1_kernel<<<grid_for(static_cast<size_t>(w.K_pad) * r, 256, sms), 256, 0, st>>>(
+        reinterpret_cast<const __nv_bfloat16*>(L1s_kr), K, w.K_pad, r, static_cast<__nv_bfloat16*>(w.L1s_t));
+    if (svdq_status s = check_launch("mx::transpose_l1_kernel"); s != SVDQ_OK) return s;
+    svdq::mx::pack_l2_kernel<<<grid_for(static_cast<size_t>(N) * r, 256, sms), 256, 0, st>>>(
+        reinterpret_cast<const __nv_bfloat16*>(L2_rn), N, r, w.n_tile, w.swiglu_interleaved,
+        static_cast<__nv_bfloat16*>(w.L2_t));
+    if (svdq_status s = check_launch("mx::pack_l2_kernel"); s != SVDQ_OK) return s;
+  }
+  *out = w;
+  return SVDQ_OK;
+}
+
+svdq_status svdq_mx_weight_bind(int N, int K, int r, int swiglu, void* blob, size_t blob_bytes, svdq_mx_weight* out) {
+  if (out == nullptr || blob == nullptr) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
+  const size_t need = svdq_mx_weight_bytes(N, K, r, swiglu);
+  if (need == 0) return fail(SVDQ_ERR_UNSUPPORTED, "MXFP4 weight shape N=%d K=%d r=%d unsupported", N, K, r);
+  if (reinterpret_cast<uintptr_t>(blob) % kAlign) return fail(SVDQ_ERR_UNSUPPORTED, "blob not 256-byte aligned");
+  if (blob_bytes < need) return fail(SVDQ_ERR_INVALID_ARG, "MXFP4 weight blob %zu bytes < %zu", blob_bytes, need);
+  if (svdq_status s = mx_ready(nullptr, nullptr); s != SVDQ_OK) return s;
+  return mx_fill_weight(static_cast<uint8_t*>(blob), N, K, r, swiglu, out);
+}
+
+svdq_status svdq_mx_quantize_act(const uint16_t* X, long long ldx, const svdq_mx_weight* w, const svdq_mx_act* act,
+                                 svdq_stream_t stream) {
+  if (X == nullptr || w == nullptr || act == nullptr) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
+  if (act->K != w->K || act->r != w->r)
+    return fail(SVDQ_ERR_INVALID_ARG, "act (K=%d r=%d) does not match weight (K=%d r=%d)", act->K, act->r, w->K, w->r);
+  if (svdq_status s = check_mx_weight(w); s != SVDQ_OK) return s;
+  if (svdq_status s = check_mx_act(act); s != SVDQ_OK) return s;
+  if (!aligned16(X)) return fail(SVDQ_ERR_UNSUPPORTED, "X must be 16-byte aligned");
+  if (ldx < act->K || ldx % 8 != 0 || ldx >= (1ll << 38))
+    return fail(SVDQ_ERR_UNSUPPORTED, "row stride %lld of X: a multiple of 8 and at least K=%d", ldx, act->K);
+  int dev, sms;
+  if (svdq_status s = mx_ready(&dev, &sms); s != SVDQ_OK) return s;
+  const int r = w->r;
+  CUtensorMap tmX, tmL1;
+  std::memcpy(&tmL1, &w->tmap[2][0], sizeof(CUtensorMap));
+  if (svdq_status s = make_tmap(&tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, X, act->K, act->M,
+                                static_cast<uint64_t>(ldx) * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+      s != SVDQ_OK)
+    return s;
+  // K split over a cluster as for the NVFP4 kernel 1 (the same kernel body and resources)
+  const int m_tiles = act->M_pad / 128;
+  int csize = 1;
+  {
+    std::lock_guard<std::mutex> lk(g_dev_mu);
+    const int* mc = g_dev[dev].k1_clusters[r == 0 ? 0 : r == 16 ? 1 : r == 32 ? 2 : 3];
+    for (int c = 2; c <= 4; ++c)
+      if (m_tiles <= mc[c - 1] && act->K_pad % (64 * c) == 0) csize = c;
+  }
+  svdq::mx::ActArgs a;
+  a.inv_lambda = w->inv_lambda;
+  a.codes = static_cast<uint8_t*>(act->codes);
+  a.sf = static_cast<uint8_t*>(act->scales);
+  a.U = static_cast<__nv_bfloat16*>(act->U);
+  a.wait_ns = g_wait_ns.load();
+  a.M = act->M;
+  a.K = act->K_pad;
+  a.M_pad = act->M_pad;
+  a.k_per_cta = act->K_pad / csize;
+
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = csize;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  set_programmatic(attr[1]);
+  cfg.gridDim = dim3(m_tiles * csize, 1, 1);
+  cfg.blockDim = dim3(svdq::kQ1Threads, 1, 1);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaSuccess;
+  switch (r) {
+    case 0:
+      cfg.dynamicSmemBytes = svdq::Q1Layout<0>::kSmem;
+      e = cudaLaunchKernelEx(&cfg, svdq::quant_act_kernel<0, svdq::mx::Act>, tmX, tmL1, a);
+      break;
+    case 16:
+      cfg.dynamicSmemBytes = svdq::Q1Layout<16>::kSmem;
+      e = cudaLaunchKernelEx(&cfg, svdq::quant_act_kernel<16, svdq::mx::Act>, tmX, tmL1, a);
+      break;
+    case 32:
+      cfg.dynamicSmemBytes = svdq::Q1Layout<32>::kSmem;
+      e = cudaLaunchKernelEx(&cfg, svdq::quant_act_kernel<32, svdq::mx::Act>, tmX, tmL1, a);
+      break;
+    default:
+      cfg.dynamicSmemBytes = svdq::Q1Layout<64>::kSmem;
+      e = cudaLaunchKernelEx(&cfg, svdq::quant_act_kernel<64, svdq::mx::Act>, tmX, tmL1, a);
+      break;
+  }
+  if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, "launch of the MXFP4 quant_act_kernel failed: %s", cudaGetErrorString(e));
+  return check_launch("quant_act_kernel (MXFP4)");
+}
+
+svdq_status svdq_mx_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const uint16_t* bias, svdq_epilogue epi,
+                         void* Y, long long ldy, svdq_out_dtype out_dtype, svdq_stream_t stream) {
+  if (act == nullptr || w == nullptr || Y == nullptr) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
+  if (act->K != w->K || act->r != w->r) return fail(SVDQ_ERR_INVALID_ARG, "act does not match weight");
+  if (svdq_status s = check_mx_weight(w); s != SVDQ_OK) return s;
+  if (svdq_status s = check_mx_act(act); s != SVDQ_OK) return s;
+  if (epi < SVDQ_EPI_NONE || epi > SVDQ_EPI_BIAS_SWIGLU) return fail(SVDQ_ERR_INVALID_ARG, "bad epilogue %d", epi);
+  if (out_dtype != SVDQ_OUT_BF16 && out_dtype != SVDQ_OUT_F32) return fail(SVDQ_ERR_INVALID_ARG, "bad out dtype");
+  const bool has_bias = (epi & 1) != 0, swiglu = (epi & 2) != 0;
+  if (has_bias && bias == nullptr) return fail(SVDQ_ERR_INVALID_ARG, "epilogue needs a bias");
+  if (swiglu && !w->swiglu_interleaved) return fail(SVDQ_ERR_INVALID_ARG, "SwiGLU needs a weight packed with swiglu=1");
+  if (!swiglu && w->swiglu_interleaved) return fail(SVDQ_ERR_INVALID_ARG, "weight packed for SwiGLU");
+  const int n_out = swiglu ? w->N / 2 : w->N;
+  const int esize = out_dtype == SVDQ_OUT_F32 ? 4 : 2;
+  if (!aligned16(Y) || (bias != nullptr && !aligned16(bias))) return fail(SVDQ_ERR_UNSUPPORTED, "Y / bias alignment");
+  if (ldy < n_out || (ldy * esize) % 16 != 0 || ldy >= (1ll << 37))
+    return fail(SVDQ_ERR_UNSUPPORTED, "row stride %lld of Y: whole 16-byte units and at least %d", ldy, n_out);
+  int dev, sms;
+  if (svdq_status s = mx_ready(&dev, &sms); s != SVDQ_OK) return s;
+
+  const int r = w->r, n_tile = w->n_tile;
+  CUtensorMap tmA, tmU, tmB, tmL2, tmY;
+  std::memset(&tmU, 0, sizeof(tmU));
+  if (svdq_status s = make_tmap(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, act->codes, act->K_pad / 2, act->M_pad,
+                                act->K_pad / 2, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+      s != SVDQ_OK)
+    return s;
+  if (r > 0) {
+    if (svdq_status s = make_tmap(&tmU, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act->U, r, 2 * static_cast<uint64_t>(act->M_pad),
+                                  static_cast<uint64_t>(r) * 2, r < 32 ? r : 32, 128, lr_swizzle(r));
+        s != SVDQ_OK)
+      return s;
+  }
+  std::memcpy(&tmB, &w->tmap[0][0], sizeof(CUtensorMap));
+  std::memcpy(&tmL2, &w->tmap[1][0], sizeof(CUtensorMap));
+  // columns past n_out and rows past M are clipped by the store
+  if (svdq_status s = make_tmap(&tmY, esize == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Y,
+                                n_out, act->M, static_cast<uint64_t>(ldy) * esize, 32, 32,
+                                esize == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+      s != SVDQ_OK)
+    return s;
+
+  svdq::mx::GemmArgs g{};
+  g.sfa = static_cast<const uint8_t*>(act->scales);
+  g.sfb = static_cast<const uint8_t*>(w->scales);
+  g.bias = reinterpret_cast<const __nv_bfloat16*>(bias);
+  g.wait_ns = g_wait_ns.load();
+  g.M = act->M;
+  g.M_pad = act->M_pad;
+  g.N = w->N;
+  g.K = w->K_pad;
+  g.r = r;
+  g.m_tiles = act->M_pad / 128;
+  g.m_pairs = (g.m_tiles + 1) / 2;
+  g.n_tiles = w->N_pad / n_tile;
+  g.k_iters = w->K_pad / 256;
+  g.num_tiles = g.m_pairs * g.n_tiles;
+  g.out_f32 = esize == 4 ? 1 : 0;
+  g.epi = static_cast<int>(epi);
+  int max_pairs = 0;
+  {
+    std::lock_guard<std::mutex> lk(g_dev_mu);
+    max_pairs = g_mx[dev].max_pairs[n_tile == 384 ? 0 : n_tile == 256 ? 1 : 2];
+  }
+  const int pairs = g.num_tiles < max_pairs ? g.num_tiles : max_pairs;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (n_tile == 384)
+    e = launch_pair_gemm(svdq::pair_gemm_kernel<svdq::mx::Gemm, 384, kMxStages384>, 2 * pairs,
+                         MxLayout<384, kMxStages384>::kSmem, st, tmA, tmB, tmU, tmL2, tmY, g);
+  else if (n_tile == 256)
+    e = launch_pair_gemm(svdq::pair_gemm_kernel<svdq::mx::Gemm, 256, kMxStages256>, 2 * pairs,
+                         MxLayout<256, kMxStages256>::kSmem, st, tmA, tmB, tmU, tmL2, tmY, g);
+  else
+    e = launch_pair_gemm(svdq::pair_gemm_kernel<svdq::mx::Gemm, 128, kMxStages128>, 2 * pairs,
+                         MxLayout<128, kMxStages128>::kSmem, st, tmA, tmB, tmU, tmL2, tmY, g);
+  if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, "launch of pair_gemm_kernel failed: %s", cudaGetErrorString(e));
+  return check_launch("pair_gemm_kernel (MXFP4)");
+}
+
+svdq_status svdq_mx_export_weight(const svdq_mx_weight* w, uint8_t* codes, uint8_t* scales, svdq_stream_t stream) {
+  if (w == nullptr || codes == nullptr || scales == nullptr) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
+  if (svdq_status s = check_mx_weight(w); s != SVDQ_OK) return s;
+  if (reinterpret_cast<uintptr_t>(codes) & 3u) return fail(SVDQ_ERR_UNSUPPORTED, "codes must be 4-byte aligned");
+  int dev, sms;
+  if (svdq_status s = mx_ready(&dev, &sms); s != SVDQ_OK) return s;
+  svdq::mx::export_kernel<<<grid_for(static_cast<size_t>(w->N) * (w->K / 8), 256, sms), 256, 0,
+                            static_cast<cudaStream_t>(stream)>>>(
+      static_cast<const uint8_t*>(w->codes), static_cast<const uint8_t*>(w->scales), w->N, w->K, w->K_pad, w->n_tile,
+      w->swiglu_interleaved, codes, scales);
+  return check_launch("mx::export_kernel");
+}
+
+svdq_status svdq_mx_export_act(const svdq_mx_act* act, uint8_t* codes, uint8_t* scales, svdq_stream_t stream) {
+  if (act == nullptr || codes == nullptr || scales == nullptr) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
+  if (svdq_status s = check_mx_act(act); s != SVDQ_OK) return s;
+  if (reinterpret_cast<uintptr_t>(codes) & 3u) return fail(SVDQ_ERR_UNSUPPORTED, "codes must be 4-byte aligned");
+  int dev, sms;
+  if (svdq_status s = mx_ready(&dev, &sms); s != SVDQ_OK) return s;
+  svdq::mx::export_kernel<<<grid_for(static_cast<size_t>(act->M) * (act->K / 8), 256, sms), 256, 0,
+                            static_cast<cudaStream_t>(stream)>>>(
+      static_cast<const uint8_t*>(act->codes), static_cast<const uint8_t*>(act->scales), act->M, act->K, act->K_pad, 0,
+      0, codes, scales);
+  return check_launch("mx::export_kernel");
+}
+
+svdq_status svdq_mx_dequantize_act(const svdq_mx_act* act, void* out, long long ld, svdq_out_dtype out_dtype,
+                                   svdq_stream_t stream) {
+  if (act == nullptr || out == nullptr) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
+  if (svdq_status s = check_mx_act(act); s != SVDQ_OK) return s;
+  if (out_dtype != SVDQ_OUT_BF16 && out_dtype != SVDQ_OUT_F32) return fail(SVDQ_ERR_INVALID_ARG, "bad out dtype");
+  if (!aligned16(out)) return fail(SVDQ_ERR_UNSUPPORTED, "out must be 16-byte aligned");
+  if (ld < act->K || ld % 8 != 0)
+    return fail(SVDQ_ERR_UNSUPPORTED, "row stride %lld of out: a multiple of 8 and at least K=%d", ld, act->K);
+  int dev, sms;
+  if (svdq_status s = mx_ready(&dev, &sms); s != SVDQ_OK) return s;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  set_programmatic(attr[0]);
+  cfg.gridDim = dim3(grid_for(static_cast<size_t>(act->M) * (act->K / 8), 256, sms), 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto* kern = out_dtype == SVDQ_OUT_F32 ? svdq::mx::dequantize_act_kernel<true> : svdq::mx::dequantize_act_kernel<false>;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<const uint8_t*>(act->codes),
+                                           static_cast<const uint8_t*>(act->scales), act->M, act->K, act->K_pad, out, ld);
+  if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, "launch of mx::dequantize_act_kernel failed: %s", cudaGetErrorString(e));
+  return check_launch("mx::dequantize_act_kernel");
+}
+
+}  // extern "C"
+
+// ================================================================== block norms
+namespace {
+
+constexpr int kNormMaxD = 32768;
+
+bool bad_norm(const svdq_norm& n) {
+  return n.kind < SVDQ_NORM_NONE || n.kind > SVDQ_NORM_LAYER || (n.f32 != 0 && n.f32 != 1) ||
+         (n.kind != SVDQ_NORM_NONE && !(n.eps >= 0.0f));
+}
+bool misaligned(const void* p, int f32) { return (reinterpret_cast<uintptr_t>(p) & (f32 ? 3u : 1u)) != 0; }
+
+// Byte range of M rows of D elements with row stride ld.
+struct Span {
+  uintptr_t lo, hi;
+  Span(const void* p, long long M, long long D, long long ld, int esize)
+      : lo(reinterpret_cast<uintptr_t>(p)), hi(lo + static_cast<uintptr_t>(((M - 1) * ld + D) * esize)) {}
+  bool overlaps(const Span& o) const { return lo < o.hi && o.lo < hi; }
+};
+
+svdq_status check_norm_args(const svdq_block_norm_args* a, bool quant) {
+  if (a == nullptr || a->x == nullptr) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
+  if (a->M < 0 || a->M >= (1 << 24) || a->D < 1) return fail(SVDQ_ERR_INVALID_ARG, "block norm of %d rows of %d", a->M, a->D);
+  if (a->D > kNormMaxD) return fail(SVDQ_ERR_UNSUPPORTED, "block norm rows of %d values (at most %d)", a->D, kNormMaxD);
+  const int flags[] = {a->x_f32, a->y_f32, a->h_f32, a->mod_f32};
+  for (int f : flags)
+    if (f != 0 && f != 1) return fail(SVDQ_ERR_INVALID_ARG, "a type flag is neither 0 nor 1");
+  if (a->samples < 1 || (a->offsets == nullptr && a->rows_per_sample < 1))
+    return fail(SVDQ_ERR_INVALID_ARG, "block norm of %d samples of %d rows", a->samples, a->rows_per_sample);
+  if (a->offsets == nullptr && a->M > 0 && (a->M - 1) / a->rows_per_sample >= a->samples)
+    return fail(SVDQ_ERR_INVALID_ARG, "%d rows are more than %d samples of %d", a->M, a->samples, a->rows_per_sample);
+  if (bad_norm(a->post) || bad_norm(a->norm)) return fail(SVDQ_ERR_INVALID_ARG, "bad norm kind, eps or type flag");
+  const bool wants_h = quant || a->h != nullptr;
+  if (wants_h != (a->norm.kind != SVDQ_NORM_NONE))
+    return fail(SVDQ_ERR_INVALID_ARG, wants_h ? "h without a norm" : "a norm without h");
+  if (!wants_h && (a->scale != nullptr || a->shift != nullptr))
+    return fail(SVDQ_ERR_INVALID_ARG, "scale and shift without h");
+  if (a->y == nullptr && (a->x_out != nullptr || a->gate != nullptr || a->post.kind != SVDQ_NORM_NONE))
+    return fail(SVDQ_ERR_INVALID_ARG, "x_out, gate or a post norm without y");
+  if (!wants_h && a->x_out == nullptr) return fail(SVDQ_ERR_INVALID_ARG, "no output");
+  const long long lds[] = {a->ldx, a->y ? a->ldy : a->D, a->x_out ? a->ld_out : a->D, a->h ? a->ldh : a->D};
+  for (long long ld : lds)
+    if (ld < a->D || ld >= (1ll << 38)) return fail(SVDQ_ERR_INVALID_ARG, "row stride %lld for rows of %d", ld, a->D);
+  const long long mods[] = {a->gate ? a->ld_gate : 0, a->scale ? a->ld_scale : 0, a->shift ? a->ld_shift : 0};
+  for (long long ld : mods)
+    if (ld < 0 || ld >= (1ll << 38)) return fail(SVDQ_ERR_INVALID_ARG, "sample stride %lld", ld);
+  if (misaligned(a->x, a->x_f32) || misaligned(a->y, a->y_f32) || misaligned(a->x_out, a->x_f32) ||
+      misaligned(a->h, a->h_f32) || misaligned(a->gate, a->mod_f32) || misaligned(a->scale, a->mod_f32) ||
+      misaligned(a->shift, a->mod_f32) || misaligned(a->post.weight, a->post.f32) ||
+      misaligned(a->post.bias, a->post.f32) || misaligned(a->norm.weight, a->norm.f32) ||
+      misaligned(a->norm.bias, a->norm.f32) || misaligned(a->offsets, 1))
+    return fail(SVDQ_ERR_UNSUPPORTED, "a pointer is not aligned to its element");
+  if (a->M > 0) {
+    // rows are read once, by the threads that write x_out's: x_out may be x, nothing else may overlap
+    const Span x(a->x, a->M, a->D, a->ldx, a->x_f32 ? 4 : 2);
+    if (a->x_out != nullptr) {
+      const Span o(a->x_out, a->M, a->D, a->ld_out, a->x_f32 ? 4 : 2);
+      if (o.overlaps(x) && !(a->x_out == a->x && a->ld_out == a->ldx))
+        return fail(SVDQ_ERR_INVALID_ARG, "x_out overlaps x without being x");
+      if (o.overlaps(Span(a->y, a->M, a->D, a->ldy, a->y_f32 ? 4 : 2)))
+        return fail(SVDQ_ERR_INVALID_ARG, "x_out overlaps y");
+    }
+    if (a->h != nullptr) {
+      const Span h(a->h, a->M, a->D, a->ldh, a->h_f32 ? 4 : 2);
+      if (h.overlaps(x) || (a->y != nullptr && h.overlaps(Span(a->y, a->M, a->D, a->ldy, a->y_f32 ? 4 : 2))) ||
+          (a->x_out != nullptr && h.overlaps(Span(a->x_out, a->M, a->D, a->ld_out, a->x_f32 ? 4 : 2))))
+        return fail(SVDQ_ERR_INVALID_ARG, "h overlaps x, y or x_out");
+    }
+  }
+  return SVDQ_OK;
+}
+
+// Every row and vector starts on a 16-byte boundary and holds whole groups of 8: the 16-byte path.
+bool norm_vectorised(const svdq_block_norm_args* a) {
+  if (a->D % 8 != 0) return false;
+  const struct { const void* p; long long ld; int f32; } rows[] = {
+      {a->x, a->ldx, a->x_f32},         {a->y, a->ldy, a->y_f32},          {a->x_out, a->ld_out, a->x_f32},
+      {a->h, a->ldh, a->h_f32},         {a->gate, a->ld_gate, a->mod_f32}, {a->scale, a->ld_scale, a->mod_f32},
+      {a->shift, a->ld_shift, a->mod_f32}, {a->post.weight, 0, 0},         {a->post.bias, 0, 0},
+      {a->norm.weight, 0, 0},           {a->norm.bias, 0, 0}};
+  for (const auto& v : rows)
+    if (v.p != nullptr && (!aligned16(v.p) || (v.ld * (v.f32 ? 4 : 2)) % 16 != 0)) return false;
+  return true;
+}
+
+svdq::norm::Norm to_norm(const svdq_norm& n) {
+  svdq::norm::Norm o{};
+  o.kind = n.kind;
+  o.eps = n.eps;
+  o.w = {n.weight, 0, n.f32};
+  o.b = {n.bias, 0, n.f32};
+  return o;
+}
+
+template <bool VEC, bool QUANT>
+cudaError_t launch_norm(const cudaLaunchConfig_t& cfg, int chunks, const svdq::norm::Args& k, int G) {
+  switch (chunks) {
+    case 1: return cudaLaunchKernelEx(&cfg, svdq::norm::block_norm_kernel<1, VEC, QUANT>, k, G);
+    case 2: return cudaLaunchKernelEx(&cfg, svdq::norm::block_norm_kernel<2, VEC, QUANT>, k, G);
+    case 3: return cudaLaunchKernelEx(&cfg, svdq::norm::block_norm_kernel<3, VEC, QUANT>, k, G);
+    case 4: return cudaLaunchKernelEx(&cfg, svdq::norm::block_norm_kernel<4, VEC, QUANT>, k, G);
+    default: return cudaLaunchKernelEx(&cfg, svdq::norm::block_norm_kernel<8, VEC, QUANT>, k, G);
+  }
+}
+
+svdq_status run_norm(const svdq_block_norm_args* a, const svdq_mx_weight* w, const svdq_mx_act* act, bool vec,
+                     int sms, svdq_stream_t stream) {
+  svdq::norm::Args k{};
+  k.x = a->x;
+  k.y = a->y;
+  k.x_out = a->x_out;
+  k.h = a->h;
+  k.ldx = a->ldx;
+  k.ldy = a->ldy;
+  k.ld_out = a->ld_out;
+  k.ldh = a->ldh;
+  k.x_f32 = a->x_f32;
+  k.y_f32 = a->y_f32;
+  k.h_f32 = a->h_f32;
+  k.M = a->M;
+  k.D = a->D;
+  k.rows = act ? act->M_pad : a->M;
+  k.samples = a->samples;
+  k.rows_per_sample = a->rows_per_sample;
+  k.offsets = a->offsets;
+  k.skip = a->skip_scale;
+  k.res = a->res_scale;
+  k.gate = {a->gate, a->ld_gate, a->mod_f32};
+  k.scale = {a->scale, a->ld_scale, a->mod_f32};
+  k.shift = {a->shift, a->ld_shift, a->mod_f32};
+  k.post = to_norm(a->post);
+  k.pre = to_norm(a->norm);
+  if (act) {
+    k.inv_lambda = w->inv_lambda;
+    k.codes = static_cast<uint8_t*>(act->codes);
+    k.sf = static_cast<uint8_t*>(act->scales);
+    k.K_pad = act->K_pad;
+  }
+  // threads per row: the fewest of 32 .. 512 that hold a row in at most 4 chunks of 8 per thread
+  const int eights = ((act ? act->K_pad : a->D) + 7) / 8;
+  int G = 32;
+  while (G < 512 && eights > 4 * G) G *= 2;
+  int chunks = (eights + G - 1) / G;
+  if (chunks > 4) chunks = 8;
+  const int block = G < 128 ? 128 : G;
+  const int per_block = block / G;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  set_programmatic(attr[0]);
+  cfg.gridDim = dim3(grid_for(k.rows, per_block, sms), 1, 1);
+  cfg.blockDim = dim3(block, 1, 1);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = act ? launch_norm<true, true>(cfg, chunks, k, G)
+                            : vec ? launch_norm<true, false>(cfg, chunks, k, G) : launch_norm<false, false>(cfg, chunks, k, G);
+  if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, "launch of norm::block_norm_kernel failed: %s", cudaGetErrorString(e));
+  return check_launch("norm::block_norm_kernel");
+}
+
+}  // namespace
+
+extern "C" {
+
+svdq_status svdq_block_norm(const svdq_block_norm_args* a, svdq_stream_t stream) {
+  if (svdq_status s = check_norm_args(a, false); s != SVDQ_OK) return s;
+  int dev, sms;
+  if (svdq_status s = device_ready(&dev, &sms); s != SVDQ_OK) return s;
+  if (a->M == 0) return SVDQ_OK;
+  return run_norm(a, nullptr, nullptr, norm_vectorised(a), sms, stream);
+}
+
+svdq_status svdq_block_norm_quantize_mx(const svdq_block_norm_args* a, const svdq_mx_weight* w, const svdq_mx_act* act,
+                                        svdq_stream_t stream) {
+  if (w == nullptr || act == nullptr) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
+  if (svdq_status s = check_norm_args(a, true); s != SVDQ_OK) return s;
+  if (svdq_status s = check_mx_weight(w); s != SVDQ_OK) return s;
+  if (svdq_status s = check_mx_act(act); s != SVDQ_OK) return s;
+  if (act->M != a->M || act->K != a->D || w->K != a->D)
+    return fail(SVDQ_ERR_INVALID_ARG, "act (M=%d K=%d) and weight (K=%d) do not match %d rows of %d", act->M, act->K,
+                w->K, a->M, a->D);
+  if (act->r != 0 || w->r != 0)
+    return fail(SVDQ_ERR_UNSUPPORTED, "a branch of rank %d projects h: use svdq_block_norm and svdq_mx_quantize_act",
+                w->r ? w->r : act->r);
+  if (!norm_vectorised(a)) return fail(SVDQ_ERR_UNSUPPORTED, "a quantized output needs 16-byte aligned rows and vectors");
+  int dev, sms;
+  if (svdq_status s = mx_ready(&dev, &sms); s != SVDQ_OK) return s;
+  return run_norm(a, w, act, true, sms, stream);
 }
 
 }  // extern "C"

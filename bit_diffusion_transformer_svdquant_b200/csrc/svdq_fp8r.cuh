@@ -229,6 +229,7 @@ struct GemmArgs {
 struct Fp8Gemm {
   using Args = GemmArgs;
   static constexpr bool kScales = false;
+  static constexpr int kSfAtomsK = 4;  // of no effect without scale factors
   static constexpr bool kL2HiLo = true;
   // the four MMAs of a 128-element K step (each K = 32, 32 bytes of codes per row)
   template <int N_TILE, int SF_ATOMS_B>

@@ -65,16 +65,18 @@ struct GemmArgs {
   int ldy, out_f32, epi;                              // epi bit 0: bias, bit 1: SwiGLU
 };
 
-// Shared memory and TMEM layout of the pair GEMM. SCALES: the block-scaled NVFP4 format, whose
-// ring slots also carry the K step's scale atoms and whose scale factors sit in TMEM buffers.
-template <bool SCALES, int N_TILE, int STAGES>
+// Shared memory and TMEM layout of the pair GEMM. SCALES: a block-scaled format, whose ring slots
+// also carry the K step's scale atoms and whose scale factors sit in TMEM buffers. SF_K: atoms of
+// 128 rows x 4 scales that a 256-wide K step takes per 128 rows (4 at one scale per 16 elements, 2 at
+// one per 32).
+template <bool SCALES, int N_TILE, int STAGES, int SF_K = 4>
 struct PairGemmLayout {
   static constexpr int kBRows = N_TILE / 2;  // rows of B staged by each CTA of the pair
   static constexpr int kA = 128 * 128;       // 128 rows x 128 bytes of codes (one K step)
   static constexpr int kB = kBRows * 128;
   static constexpr int kSfAtomsB = (N_TILE + 127) / 128;
-  static constexpr int kSfa = SCALES ? 4 * 512 : 0;
-  static constexpr int kSfb = SCALES ? 4 * kSfAtomsB * 512 : 0;
+  static constexpr int kSfa = SCALES ? SF_K * 512 : 0;
+  static constexpr int kSfb = SCALES ? SF_K * kSfAtomsB * 512 : 0;
   static constexpr int kStage = kA + kB + kSfa + kSfb;
   static constexpr int kOffB = kA;
   static constexpr int kOffSfa = kA + kB;
@@ -82,10 +84,10 @@ struct PairGemmLayout {
   // a low-rank slot holds U_hi (offset 0), U_lo (kOffULo), this CTA's half of L2^T (kOffB) and, for
   // a format whose L2^T is kept as a bf16 hi/lo pair, its lo half (kOffL2Lo)
   static constexpr int kOffL2Lo = kOffB + kBRows * 32 * 2;
-  // TMEM scale-factor buffer (one K step): SFA 4 MMAs x 4 columns, then SFB 4 MMAs x 4 x atoms.
-  // Four buffers beside an accumulator of up to 256 columns; two beside the 384-column one.
-  static constexpr int kSfCols = SCALES ? 16 + 16 * kSfAtomsB : 0;
-  static constexpr int kSfBufs = SCALES ? (N_TILE > 256 ? 2 : 4) : 0;
+  // TMEM scale-factor buffer (one K step): SFA SF_K atoms x 4 columns, then SFB SF_K x 4 x atoms.
+  // Four buffers where they fit beside the accumulator, else two (NVFP4's 384-column tile).
+  static constexpr int kSfCols = SCALES ? 4 * SF_K * (1 + kSfAtomsB) : 0;
+  static constexpr int kSfBufs = SCALES ? (N_TILE + 4 * kSfCols <= 512 ? 4 : 2) : 0;
   static constexpr int kAccBufs = (2 * N_TILE + kSfBufs * kSfCols <= 512) ? 2 : 1;
   static constexpr int kColSf = kAccBufs * N_TILE;  // kSfBufs buffers of kSfCols columns from here
   // epilogue staging: 8 warps x 4 KB (two 32 x 32 bf16 boxes or one fp32 box in flight)
@@ -101,7 +103,8 @@ struct PairGemmLayout {
   static_assert(kColSf + kSfBufs * kSfCols <= 512, "TMEM budget");
   static_assert(kSfBufs <= STAGES, "a scale buffer's previous slot must still own its ring stage");
   static_assert(kSmem <= 232448, "shared memory budget");
-  static_assert(N_TILE <= 256 || (SCALES && N_TILE == 384), "the 384-wide tile is an NVFP4 tile");
+  static_assert(N_TILE <= 256 || (SCALES && N_TILE == 384), "the 384-wide tile is a block-scaled FP4 tile");
+  static_assert(SF_K == 4 || SF_K == 2, "one scale per 16 or 32 elements");
 };
 template <int N_TILE, int STAGES>
 using GemmLayout = PairGemmLayout<true, N_TILE, STAGES>;
@@ -119,6 +122,11 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint4 (&v)[4])
       "r"(v[0].x), "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z), "r"(v[1].w),
       "r"(v[2].x), "r"(v[2].y), "r"(v[2].z), "r"(v[2].w), "r"(v[3].x), "r"(v[3].y), "r"(v[3].z), "r"(v[3].w)
       : "memory");
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint4 (&v)[2]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0].x),
+               "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z), "r"(v[1].w)
+               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_id_x() {
@@ -139,6 +147,7 @@ __device__ __forceinline__ uint32_t num_clusters_x() {
 struct Nvfp4Gemm {
   using Args = GemmArgs;
   static constexpr bool kScales = true;
+  static constexpr int kSfAtomsK = 4;
   static constexpr bool kL2HiLo = false;
   // the MMAs of a 256-element K step: four of K = 64 (32 bytes of codes per row); the SFA of MMA j
   // at tsf + 4j, its SFB atoms (128 tile columns each) from tsf + 16 + 4 SF_ATOMS_B j on
@@ -212,7 +221,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     pair_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmL2,
                      const __grid_constant__ CUtensorMap tmY, const typename F::Args args) {
-  using L = PairGemmLayout<F::kScales, N_TILE, STAGES>;
+  constexpr int kSfK = F::kSfAtomsK;
+  using L = PairGemmLayout<F::kScales, N_TILE, STAGES, kSfK>;
   constexpr int kSfBufs = L::kSfBufs, kAccBufs = L::kAccBufs;
   extern __shared__ uint8_t smem_raw[];
   // the same offsets in both CTAs: the pair MMA addresses the odd CTA's operands by this CTA's
@@ -285,7 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       uint32_t phase = 0, armed = 0, armed_parity = 0;
       const int rc = r < kLrChunk ? r : kLrChunk;
       const uint32_t lr_bytes = static_cast<uint32_t>((2 * 128 + (F::kL2HiLo ? 2 : 1) * L::kBRows) * rc * 2);
-      const int sf_row_stride = args.K >> 6;  // 64-wide K atoms per 128-row block
+      const int sf_row_stride = (args.K >> 8) * kSfK;  // scale atoms per 128-row block
       const bool leader = rank == 0;
       bool ok = true;
       for (int tile = pair0; ok && tile < args.num_tiles; tile += npairs) {
@@ -320,8 +330,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             const uint8_t* sfa_tile = args.sfa + (static_cast<size_t>(m_sf) * sf_row_stride << 9);
             const uint8_t* sfb_tile = args.sfb + (static_cast<size_t>(n_blk) * sf_row_stride * L::kSfAtomsB << 9);
             mbar_arrive_expect_tx(sf_land_bar(stage), L::kSfa + L::kSfb);
-            bulk_load(sa + L::kOffSfa, sfa_tile + (static_cast<size_t>(kt) * 4 << 9), L::kSfa, sf_land_bar(stage));
-            bulk_load(sa + L::kOffSfb, sfb_tile + (static_cast<size_t>(kt) * 4 * L::kSfAtomsB << 9), L::kSfb,
+            bulk_load(sa + L::kOffSfa, sfa_tile + (static_cast<size_t>(kt) * kSfK << 9), L::kSfa, sf_land_bar(stage));
+            bulk_load(sa + L::kOffSfb, sfb_tile + (static_cast<size_t>(kt) * kSfK * L::kSfAtomsB << 9), L::kSfb,
                       sf_land_bar(stage));
           } else {
             (void)m_sf;
@@ -454,13 +464,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           if (!__all_sync(0xffffffffu, got_data)) { ok = false; break; }
           const bool has_sf = slot >= lr_slots;
           // read the stage's scale atoms now; only the TMEM stores wait for the buffer
-          uint4 fa[4], fb[4 * L::kSfAtomsB];
+          uint4 fa[kSfK], fb[kSfK * L::kSfAtomsB];
           if (has_sf) {
             const uint8_t* sfs = smem + stage * L::kStage + L::kOffSfa + lane * 16;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) fa[i] = *reinterpret_cast<const uint4*>(sfs + 512 * i);
+            for (int i = 0; i < kSfK; ++i) fa[i] = *reinterpret_cast<const uint4*>(sfs + 512 * i);
 #pragma unroll
-            for (int i = 0; i < 4 * L::kSfAtomsB; ++i)
+            for (int i = 0; i < kSfK * L::kSfAtomsB; ++i)
               fb[i] = *reinterpret_cast<const uint4*>(smem + stage * L::kStage + L::kOffSfb + lane * 16 + 512 * i);
           }
           // Every slot, with scales or not, first waits for the release of the slot kSfBufs back
@@ -481,11 +491,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           if (has_sf) {
             tc_fence_after();
             const uint32_t tsf = tmem + (static_cast<uint32_t>(q * 32) << 16) + L::kColSf + sfb * L::kSfCols;
-            tmem_st_x16(tsf, fa);
+            if constexpr (kSfK == 4) {
+              tmem_st_x16(tsf, fa);
 #pragma unroll
-            for (int h = 0; h < L::kSfAtomsB; ++h) {
-              const uint4 v[4] = {fb[4 * h], fb[4 * h + 1], fb[4 * h + 2], fb[4 * h + 3]};
-              tmem_st_x16(tsf + 16 + 16 * h, v);
+              for (int h = 0; h < L::kSfAtomsB; ++h) {
+                const uint4 v[4] = {fb[4 * h], fb[4 * h + 1], fb[4 * h + 2], fb[4 * h + 3]};
+                tmem_st_x16(tsf + 16 + 16 * h, v);
+              }
+            } else {
+              tmem_st_x8(tsf, fa);
+#pragma unroll
+              for (int h = 0; h < L::kSfAtomsB; ++h) {
+                const uint4 v[2] = {fb[2 * h], fb[2 * h + 1]};
+                tmem_st_x8(tsf + 8 + 8 * h, v);
+              }
             }
             tmem_wait_st();
           }

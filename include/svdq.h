@@ -20,9 +20,10 @@
  *                         256-row tile (TMA-fed shared-memory rings, TMEM accumulators) whose
  *                         epilogue adds the up-projection U L2 (bf16 MMAs into the same
  *                         accumulator), bias and SwiGLU before one store.
- * Further down: the row-wise FP8 (W8A8) variant of the same layer (svdq_fp8r_*), and the MLP
+ * Further down: the row-wise FP8 (W8A8) variant of the same layer (svdq_fp8r_*), the MLP
  * chain's call that fuses the down layer's activation quantization into the gate/up GEMM's
- * SwiGLU epilogue (svdq_gemm_swiglu_quant).
+ * SwiGLU epilogue (svdq_gemm_swiglu_quant), the MXFP4 variant (svdq_mx_*), and the norms, gate and
+ * residual between layers (svdq_block_norm*).
  *
  * Conventions for every entry point:
  *   - Pointers named as device memory must be device pointers on the current device; the library
@@ -299,6 +300,135 @@ SVDQ_API svdq_status svdq_gemm_swiglu_quant_noscratch(const svdq_act* act, const
                                                       const uint16_t* bias, const svdq_weight* w_next,
                                                       const float* g_x_next, const svdq_act* act_next,
                                                       uint16_t* H, svdq_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * MXFP4 variant: the same layer with the microscaled 4-bit format of the OCP "Microscaling Formats
+ * (MX)" specification v1.0: E2M1 elements, one power-of-two scale (E8M0) per 32 elements along K,
+ * no tensor scale and so no calibration. Quantization of a block of 32 fp32 values v:
+ *   e = floor(log2(max |v|)) - 2, at least -127 (-127 for an all-zero block);  scale code = e + 127;
+ *   q = E2M1_rne_sat(v 2^-e)     (round to nearest, ties to the even code, saturating at 6)
+ * a block that holds an infinity or a NaN gets scale code 255 (E8M0's NaN) and zero codes, so every
+ * output that reads it is NaN. Activations are quantized from x_hat = fp32(x * inv_lambda).
+ *   y = sum_k dec(qx) 2^ex dec(qw) 2^ew  +  (X L1s) L2  (+ bias)   [then SwiGLU]
+ * Conventions as above, with wider shapes: K % 8 == 0, N % 8 == 0 (SwiGLU: N % 16 == 0), any M >= 1,
+ * and row strides for X and Y. The buffers are padded: K_pad = K up to a multiple of 256, N_pad = N
+ * up to whole GEMM tiles; padding holds zero codes. */
+typedef struct svdq_mx_weight {
+  int N, K, r;
+  int swiglu_interleaved; /* 1: gate/up rows interleaved per n_tile (256)                       */
+  int n_tile;             /* GEMM tile width along N: 384, 256 or 128                           */
+  int N_pad, K_pad;
+  int reserved0;
+  void* codes;            /* uint8 [N_pad][K_pad/2] E2M1 codes, rows in GEMM order               */
+  void* scales;           /* E8M0 scales in the per-n_tile MMA layout                            */
+  float* inv_lambda;      /* device fp32 [K_pad] smoothing reciprocals (1 in the padding)        */
+  void* L1s_t;            /* bf16 [r][K_pad] = (diag(lambda)^-1 L1)^T                            */
+  void* L2_t;             /* bf16 [N_pad][r] = L2^T, rows in GEMM order                          */
+  unsigned long long tmap[3][16]; /* opaque: cached TMA descriptors of codes, L2_t and L1s_t     */
+} svdq_mx_weight;
+
+typedef struct svdq_mx_act {
+  int M, K, r, M_pad, K_pad; /* M_pad = M up to a multiple of 128                                */
+  int reserved0;
+  void* codes;            /* uint8 [M_pad][K_pad/2] E2M1 codes (zero in the padding)             */
+  void* scales;           /* E8M0, [M_pad/128][K_pad/128] atoms of 512 bytes: byte               */
+                          /*   (m%32)*16 + ((m%128)/32)*4 + (k/32)%4 of atom (m/128, k/128)      */
+  void* U;                /* bf16 [2][M_pad][r]: u = fp32(X L1s) as hi = bf16(u), lo = bf16(u - hi) */
+} svdq_mx_act;
+
+/* Bytes of device memory a packed MXFP4 weight / activation needs (0 on bad shapes). */
+SVDQ_API size_t svdq_mx_weight_bytes(int N, int K, int r, int swiglu);
+SVDQ_API size_t svdq_mx_act_bytes(int M, int K, int r);
+
+/* Offline pack, arguments as svdq_pack_weight; inv_lambda may be NULL (no smoothing: all 1). */
+SVDQ_API svdq_status svdq_mx_pack_weight(const float* R_nk, const uint16_t* L1s_kr, const uint16_t* L2_rn,
+                                const float* inv_lambda, int N, int K, int r, int swiglu, void* dst,
+                                size_t dst_bytes, svdq_mx_weight* out, svdq_stream_t stream);
+
+/* Checkpoints: as svdq_weight_bind, for a blob written by svdq_mx_pack_weight with these sizes. */
+SVDQ_API svdq_status svdq_mx_weight_bind(int N, int K, int r, int swiglu, void* blob, size_t blob_bytes,
+                                svdq_mx_weight* out);
+
+/* Host-only: lay an svdq_mx_act out over `dst` (device, >= svdq_mx_act_bytes, 256-aligned). */
+SVDQ_API svdq_status svdq_mx_act_bind(int M, int K, int r, void* dst, size_t dst_bytes, svdq_mx_act* out);
+
+/* Per layer call: smoothing, MXFP4 quantization and U = X L1s in one pass over X. X: device bf16
+ * [M][K] with row stride ldx (elements, a multiple of 8, >= K). */
+SVDQ_API svdq_status svdq_mx_quantize_act(const uint16_t* X, long long ldx, const svdq_mx_weight* w,
+                                 const svdq_mx_act* act, svdq_stream_t stream);
+
+/* Per layer call: the block-scaled GEMM (tcgen05 kind::mxf4) with the branch's up-projection in the
+ * same accumulator, bias and SwiGLU. Y: device [M][N] (or [M][N/2]) of out_dtype with row stride ldy
+ * (elements; ldy * element size a multiple of 16 bytes). bias, epi and out_dtype as for svdq_gemm. */
+SVDQ_API svdq_status svdq_mx_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const uint16_t* bias,
+                         svdq_epilogue epi, void* Y, long long ldy, svdq_out_dtype out_dtype,
+                         svdq_stream_t stream);
+
+/* Debug / parity: canonical codes [rows][K/2] and scale codes [rows][ceil(K/32)] (weight rows in the
+ * original order; act rows 0..M-1). */
+SVDQ_API svdq_status svdq_mx_export_weight(const svdq_mx_weight* w, uint8_t* codes, uint8_t* scales,
+                                  svdq_stream_t stream);
+SVDQ_API svdq_status svdq_mx_export_act(const svdq_mx_act* act, uint8_t* codes, uint8_t* scales,
+                               svdq_stream_t stream);
+
+/* The values a quantized activation stands for, dec(q) 2^e (the smoothed x_hat, e.g. for calibration
+ * errors): out [M][K] of out_dtype with row stride ld (elements, a multiple of 8, >= K). fp32 holds
+ * every value exactly, bf16 every value of a scale above 2^-126. */
+SVDQ_API svdq_status svdq_mx_dequantize_act(const svdq_mx_act* act, void* out, long long ld,
+                                   svdq_out_dtype out_dtype, svdq_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Block norms: the normalisation in front of a transformer block's linear, and what ends a block --
+ * an optional norm of the block's output, its gate and the residual -- in one pass per row:
+ *   x' = skip_scale x + res_scale gate_s . P(y)            (only with y; P = post norm or identity)
+ *   h  = Norm(x') . (1 + scale_s) + shift_s                 (only with h or a quantized output; x' = x
+ *                                                            without y)
+ *   Norm(v) = (v - mean) / sqrt(var + eps) . weight + bias   (SVDQ_NORM_LAYER, var = mean((v - mean)^2))
+ *           = v / sqrt(mean(v^2) + eps) . weight (+ bias)     (SVDQ_NORM_RMS)
+ * s is the row's sample; . is elementwise; absent vectors act as 1 (weight, gate) or 0 (bias, scale,
+ * shift). Everything is computed in fp32; x' and h are rounded once, when stored (h from the unrounded
+ * x'). Rows: M rows of D values with row strides (elements). Samples: without offsets row m belongs to
+ * sample m / rows_per_sample; with offsets (device int32 [samples + 1], ascending) sample s has rows
+ * offsets[s] .. offsets[s + 1] - 1, and rows outside every sample are neither read nor written.
+ * x_out may be x itself (same stride); h must not overlap an input. 1 <= D <= 32768; any strides and
+ * element alignment (16-byte aligned rows and vectors with D a multiple of 8 take the fast path). */
+typedef enum { SVDQ_NORM_NONE = 0, SVDQ_NORM_RMS = 1, SVDQ_NORM_LAYER = 2 } svdq_norm_kind;
+
+typedef struct svdq_norm {   /* one normalisation: kind, eps and its vectors */
+  int kind;                  /* svdq_norm_kind                                   */
+  float eps;
+  int f32;                   /* weight and bias: 1 fp32, 0 bf16                  */
+  int reserved0;
+  const void* weight;        /* device [D] or NULL                               */
+  const void* bias;          /* device [D] or NULL                               */
+} svdq_norm;
+
+typedef struct svdq_block_norm_args {
+  int M, D;
+  int samples, rows_per_sample;         /* rows_per_sample >= 1 without offsets          */
+  const int32_t* offsets;               /* device, or NULL                               */
+  const void* x;  long long ldx;  int x_f32;   /* 1: fp32, 0: bf16; also x_out's type    */
+  int y_f32;      const void* y;  long long ldy;
+  void* x_out;    long long ld_out;     /* with y; NULL: x' is not stored                */
+  void* h;        long long ldh;  int h_f32;
+  int mod_f32;                          /* gate, scale and shift: 1 fp32, 0 bf16         */
+  const void* gate;  long long ld_gate; /* [samples][D] each with its own row stride     */
+  const void* scale; long long ld_scale;
+  const void* shift; long long ld_shift;
+  float skip_scale, res_scale;
+  svdq_norm post;                       /* of y; kind NONE: identity                     */
+  svdq_norm norm;                       /* of x'; kind NONE with h == NULL only          */
+} svdq_block_norm_args;
+
+SVDQ_API svdq_status svdq_block_norm(const svdq_block_norm_args* a, svdq_stream_t stream);
+
+/* The same pass with bf16(h) quantized for the next layer instead of (or beside) being stored: the
+ * codes and scales are those svdq_mx_quantize_act makes of h. `act` is bound with M = a->M, K = a->D;
+ * w supplies inv_lambda (w->K == a->D) and has no branch (w->r == 0: a branch projects h itself, so
+ * use svdq_block_norm with h and svdq_mx_quantize_act). D % 8 == 0, 16-byte aligned rows and
+ * vectors. Rows outside every sample are quantized as zero. */
+SVDQ_API svdq_status svdq_block_norm_quantize_mx(const svdq_block_norm_args* a, const svdq_mx_weight* w,
+                                        const svdq_mx_act* act, svdq_stream_t stream);
 
 SVDQ_API const char* svdq_status_str(svdq_status s);
 SVDQ_API const char* svdq_last_error(void);

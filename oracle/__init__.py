@@ -10,6 +10,8 @@ Modules:
   nvfp4     -- E2M1 / E4M3 codecs and the NVFP4 block quantizer.
   svdquant  -- smoothing factors, the low-rank/residual split, and the layer forward.
   fp8r      -- the row-wise FP8 (W8A8) variant of the same layer.
+  mxfp4     -- the MXFP4 (one power-of-two scale per 32 elements) variant of the same layer.
+  block_norm -- the norms, gate and residual around a block.
 
 Pins (what each function is checked against, in ``tests/test_oracle_*.py``):
   codecs            -- the format's printed E2M1 grid and hand-derived tie cases; a closed-form
@@ -29,5 +31,10 @@ Pins (what each function is checked against, in ``tests/test_oracle_*.py``):
                        on +-448, zero rows, the E4M3 half-ulp error bound, scale invariance under
                        power-of-two row scaling; layer: exact-rational triple loop, r=0 reducing
                        to plain W8A8.
+  mxfp4             -- power-of-two invariance, idempotence, the scale range of a block's largest
+                       element, zero / subnormal / non-finite blocks, a partial last block; layer:
+                       exact-rational triple loop.
+  block_norm        -- unit mean square and zero mean of the normalised row, invariances under
+                       shifts and scales of the row, torch's layer_norm (a library routine).
 No function here is left without a pin.
 """
