@@ -573,6 +573,8 @@ class MxAct:
         nbytes = lib().svdq_mx_act_bytes(M, K, r)
         if nbytes == 0:
             raise SvdqError("svdq_mx_act_bytes", 2, f"unsupported shape M={M} K={K} r={r}")
+        if torch.device(device).type != "cuda":
+            raise ValueError(f"device {device}: expected a CUDA device")
         self.buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.desc = SvdqMxAct()
         _check("svdq_mx_act_bind", lib().svdq_mx_act_bind(M, K, r, _ptr(self.buf), nbytes, byref(self.desc)))

@@ -1989,15 +1989,67 @@ svdq::norm::Norm to_norm(const svdq_norm& n) {
   return o;
 }
 
-template <bool VEC, bool QUANT>
-cudaError_t launch_norm(const cudaLaunchConfig_t& cfg, int chunks, const svdq::norm::Args& k, int G) {
+// The instantiations of the 16-byte kernel: C chunks of 8 per thread and R rows at a time; x's type, y's
+// (or none), a quantized output or not.
+using NormKernel = void (*)(svdq::norm::Args, int, int, int, unsigned long long);
+constexpr int norm_batch(int chunks) { return chunks == 1 ? 4 : chunks == 2 ? 2 : 1; }
+template <bool XF32, int Y, bool QUANT>
+NormKernel norm_kernel(int chunks, bool share) {
+  using namespace svdq::norm;
+  if (!share)
+    return chunks <= 2 ? block_norm_kernel<2, norm_batch(2), XF32, Y, QUANT, false>
+                       : block_norm_kernel<8, norm_batch(8), XF32, Y, QUANT, false>;
   switch (chunks) {
-    case 1: return cudaLaunchKernelEx(&cfg, svdq::norm::block_norm_kernel<1, VEC, QUANT>, k, G);
-    case 2: return cudaLaunchKernelEx(&cfg, svdq::norm::block_norm_kernel<2, VEC, QUANT>, k, G);
-    case 3: return cudaLaunchKernelEx(&cfg, svdq::norm::block_norm_kernel<3, VEC, QUANT>, k, G);
-    case 4: return cudaLaunchKernelEx(&cfg, svdq::norm::block_norm_kernel<4, VEC, QUANT>, k, G);
-    default: return cudaLaunchKernelEx(&cfg, svdq::norm::block_norm_kernel<8, VEC, QUANT>, k, G);
+    case 1: return block_norm_kernel<1, norm_batch(1), XF32, Y, QUANT, true>;
+    case 2: return block_norm_kernel<2, norm_batch(2), XF32, Y, QUANT, true>;
+    case 4: return block_norm_kernel<4, norm_batch(4), XF32, Y, QUANT, true>;
+    case 6: return block_norm_kernel<6, norm_batch(6), XF32, Y, QUANT, true>;
+    default: return block_norm_kernel<8, norm_batch(8), XF32, Y, QUANT, true>;
   }
+}
+template <bool XF32, bool QUANT>
+NormKernel norm_kernel(int chunks, bool share, int y) {
+  using namespace svdq::norm;
+  return y == kNoY    ? norm_kernel<XF32, kNoY, QUANT>(chunks, share)
+         : y == kF32Y ? norm_kernel<XF32, kF32Y, QUANT>(chunks, share)
+                      : norm_kernel<XF32, kBf16Y, QUANT>(chunks, share);
+}
+NormKernel norm_kernel(int chunks, bool share, bool x_f32, int y, bool quant) {
+  if (quant) return x_f32 ? norm_kernel<true, true>(chunks, share, y) : norm_kernel<false, true>(chunks, share, y);
+  return x_f32 ? norm_kernel<true, false>(chunks, share, y) : norm_kernel<false, false>(chunks, share, y);
+}
+cudaError_t launch_norm_any(const cudaLaunchConfig_t& cfg, int chunks, const svdq::norm::Args& k, int G) {
+  switch (chunks) {
+    case 1: return cudaLaunchKernelEx(&cfg, svdq::norm::block_norm_any_kernel<1>, k, G);
+    case 2: return cudaLaunchKernelEx(&cfg, svdq::norm::block_norm_any_kernel<2>, k, G);
+    case 4: return cudaLaunchKernelEx(&cfg, svdq::norm::block_norm_any_kernel<4>, k, G);
+    case 6: return cudaLaunchKernelEx(&cfg, svdq::norm::block_norm_any_kernel<6>, k, G);
+    default: return cudaLaunchKernelEx(&cfg, svdq::norm::block_norm_any_kernel<8>, k, G);
+  }
+}
+
+constexpr int kNormSmem = 212 * 1024;  // the most a block's rings take
+struct NormState {
+  bool ready = false;
+};
+NormState g_norm[64];
+
+svdq_status norm_setup() {
+  for (int chunks : {1, 2, 4, 6, 8})
+    for (int v = 0; v < 24; ++v)
+      SVDQ_CUDA(cudaFuncSetAttribute(norm_kernel(chunks, v >= 12, v & 1, (v >> 1) % 3, (v / 6) & 1),
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem));
+  return SVDQ_OK;
+}
+svdq_status norm_ready(int* sm_out) {
+  int dev = 0;
+  if (svdq_status s = device_ready(&dev, sm_out); s != SVDQ_OK) return s;
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  if (!g_norm[dev].ready) {
+    if (svdq_status s = norm_setup(); s != SVDQ_OK) return s;
+    g_norm[dev].ready = true;
+  }
+  return SVDQ_OK;
 }
 
 svdq_status run_norm(const svdq_block_norm_args* a, const svdq_mx_weight* w, const svdq_mx_act* act, bool vec,
@@ -2018,7 +2070,8 @@ svdq_status run_norm(const svdq_block_norm_args* a, const svdq_mx_weight* w, con
   k.D = a->D;
   k.rows = act ? act->M_pad : a->M;
   k.samples = a->samples;
-  k.rows_per_sample = a->rows_per_sample;
+  k.rows_per_sample = a->offsets ? 0 : a->rows_per_sample;
+  k.per_sample = a->offsets || a->rows_per_sample == 1 ? 0 : ~0ull / a->rows_per_sample + 1;
   k.offsets = a->offsets;
   k.skip = a->skip_scale;
   k.res = a->res_scale;
@@ -2033,24 +2086,67 @@ svdq_status run_norm(const svdq_block_norm_args* a, const svdq_mx_weight* w, con
     k.sf = static_cast<uint8_t*>(act->scales);
     k.K_pad = act->K_pad;
   }
-  // threads per row: the fewest of 32 .. 512 that hold a row in at most 4 chunks of 8 per thread
   const int eights = ((act ? act->K_pad : a->D) + 7) / 8;
-  int G = 32;
-  while (G < 512 && eights > 4 * G) G *= 2;
-  int chunks = (eights + G - 1) / G;
-  if (chunks > 4) chunks = 8;
-  const int block = G < 128 ? 128 : G;
-  const int per_block = block / G;
+  const auto whole = [](int c) { return c <= 2 ? c : c <= 4 ? 4 : c <= 6 ? 6 : 8; };
+  // warps per row for at most `most` chunks of 8 values per thread
+  const auto row_warps = [&](int most) {
+    const int w = (eights + 32 * most - 1) / (32 * most);
+    return svdq::norm::kMaxWarps / (w < svdq::norm::kMaxWarps ? svdq::norm::kMaxWarps / w : 1);  // leaves no warp over
+  };
+  int W = row_warps(6), chunks = whole((eights + 32 * W - 1) / (32 * W));
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   set_programmatic(attr[0]);
-  cfg.gridDim = dim3(grid_for(k.rows, per_block, sms), 1, 1);
-  cfg.blockDim = dim3(block, 1, 1);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = act ? launch_norm<true, true>(cfg, chunks, k, G)
-                            : vec ? launch_norm<true, false>(cfg, chunks, k, G) : launch_norm<false, false>(cfg, chunks, k, G);
+  const int elem_bytes = (a->x_f32 ? 4 : 2) + (a->y == nullptr ? 0 : a->y_f32 ? 4 : 2);
+  cudaError_t e;
+  if (vec) {
+    const auto stage_bytes = [&] { return norm_batch(chunks) * chunks * 256 * W * elem_bytes; };
+    const auto factor_bytes = [&] { return chunks * 256 * W * (a->y ? 12 : 8); };
+    // factors of a run's sample in shared memory where a run gives every group two batches; else (or
+    // where they do not fit beside a batch) two or eight chunks per thread and vectors read per row
+    const int per_run = a->offsets ? a->M / a->samples : a->rows_per_sample;
+    const bool share = per_run >= 2 * (svdq::norm::kMaxWarps / W) * norm_batch(chunks) &&
+                       stage_bytes() + factor_bytes() <= kNormSmem;
+    if (!share) {
+      W = row_warps(2);
+      chunks = (eights + 32 * W - 1) / (32 * W) <= 2 ? 2 : 8;
+    }
+    if (stage_bytes() <= kNormSmem) {
+      // Rows in flight per SM: as many groups as fit a block, but no more than about 80 KB of batches; a
+      // second stage where that leaves room for one. Measured on B200 over two samples of 16896 rows of
+      // 3072, all bf16 (12 KB of x and y): 6 groups 137 us, 8 groups 157 us, 4 groups 171 us, 6 groups with
+      // two stages 138 us; without y (6 KB) over 4608 rows: 8 groups 13.2 us, 6 groups 15.2 us, 8 groups with
+      // two stages 13.9 us; 4000 rows of 8192 without y (2 groups, 32 KB): one stage 33.8 us, two 32.1 us.
+      constexpr int kInFlight = 80 * 1024;
+      const int sets = 2 * factor_bytes() + stage_bytes() <= kNormSmem ? 2 : 1;
+      const int fixed = share ? sets * factor_bytes() : 0, R = norm_batch(chunks);
+      int groups = svdq::norm::kMaxWarps / W;
+      while (groups > 1 && (groups * stage_bytes() > kInFlight || groups * stage_bytes() + fixed > kNormSmem)) --groups;
+      const int stages = 2 * groups * stage_bytes() <= kInFlight ? 2 : 1;
+      const int batches = (k.rows + R - 1) / R, blocks = (batches + groups - 1) / groups;
+      cfg.gridDim = dim3(blocks < sms ? blocks : sms, 1, 1);
+      cfg.blockDim = dim3(groups * 32 * W, 1, 1);
+      cfg.dynamicSmemBytes = static_cast<size_t>(groups) * stages * stage_bytes() + fixed;
+      e = cudaLaunchKernelEx(
+          &cfg, norm_kernel(chunks, share, a->x_f32, a->y == nullptr ? svdq::norm::kNoY : 1 + a->y_f32, act != nullptr), k,
+          32 * W, stages, sets, g_wait_ns.load());
+      if (e != cudaSuccess)
+        return fail(SVDQ_ERR_CUDA, "launch of norm::block_norm_kernel failed: %s", cudaGetErrorString(e));
+      return check_launch("norm::block_norm_kernel");
+    }
+    if (act)
+      return fail(SVDQ_ERR_UNSUPPORTED, "rows of x and y of %d bytes (at most %d with a quantized output)", stage_bytes(),
+                  kNormSmem);
+  }
+  W = row_warps(1);
+  chunks = whole((eights + 32 * W - 1) / (32 * W));
+  const int groups = W >= 4 ? 1 : 4 / W;
+  cfg.gridDim = dim3(grid_for(k.rows, groups, sms), 1, 1);
+  cfg.blockDim = dim3(groups * 32 * W, 1, 1);
+  e = launch_norm_any(cfg, chunks, k, 32 * W);
   if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, "launch of norm::block_norm_kernel failed: %s", cudaGetErrorString(e));
   return check_launch("norm::block_norm_kernel");
 }
@@ -2061,8 +2157,8 @@ extern "C" {
 
 svdq_status svdq_block_norm(const svdq_block_norm_args* a, svdq_stream_t stream) {
   if (svdq_status s = check_norm_args(a, false); s != SVDQ_OK) return s;
-  int dev, sms;
-  if (svdq_status s = device_ready(&dev, &sms); s != SVDQ_OK) return s;
+  int sms;
+  if (svdq_status s = norm_ready(&sms); s != SVDQ_OK) return s;
   if (a->M == 0) return SVDQ_OK;
   return run_norm(a, nullptr, nullptr, norm_vectorised(a), sms, stream);
 }
@@ -2080,8 +2176,8 @@ svdq_status svdq_block_norm_quantize_mx(const svdq_block_norm_args* a, const svd
     return fail(SVDQ_ERR_UNSUPPORTED, "a branch of rank %d projects h: use svdq_block_norm and svdq_mx_quantize_act",
                 w->r ? w->r : act->r);
   if (!norm_vectorised(a)) return fail(SVDQ_ERR_UNSUPPORTED, "a quantized output needs 16-byte aligned rows and vectors");
-  int dev, sms;
-  if (svdq_status s = mx_ready(&dev, &sms); s != SVDQ_OK) return s;
+  int sms;
+  if (svdq_status s = norm_ready(&sms); s != SVDQ_OK) return s;
   return run_norm(a, w, act, true, sms, stream);
 }
 

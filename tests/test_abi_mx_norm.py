@@ -226,9 +226,8 @@ def test_binding_refuses_before_the_library(L):
         svdq.Norm("rms", eps=-1e-6)
     with pytest.raises(ValueError, match="h without a norm"):
         svdq.gated_residual(cpu, cpu, h=cpu)
-    act = svdq.MxAct(4, 64, 0, "cpu")
     with pytest.raises(ValueError, match="CUDA"):
-        svdq.dequantize_act_mx(act)
+        svdq.MxAct(4, 64, 0, "cpu")
     with pytest.raises(svdq.SvdqError, match="unsupported shape"):
         svdq.MxAct(4, 63, 0, "cpu")
     state = {"abi": L.svdq_abi_version(), "format": "mxfp4", "N": 128, "K": 256, "r": 0, "swiglu": False}
