@@ -487,15 +487,38 @@ def export_act_fp8r(act: Fp8rAct):
 
 
 # ---------------------------------------------------------------- MXFP4 variant
+# The calls of this part and the next are small enough for host time to show (a norm of a few rows takes
+# the GPU 4 us), so their checks touch each tensor few times and the device guard is entered only
+# where the tensors' device is not the current one.
 
-def _rows(t, dtype, name, dim):
-    """A CUDA matrix whose rows are contiguous (any row stride)."""
-    if not t.is_cuda or t.dtype != dtype or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _enqueue(device, *calls):
+    """Each call (entry point, arguments before the stream) on the device's current stream."""
+    index = device.index
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _enqueue(device, *calls)
+    l, stream = _lib or lib(), _raw_stream(index)
+    for name, *args in calls:
+        status = getattr(l, name)(*args, stream)
+        if status:
+            _check(name, status)
+
+
+def _rows(t, dtype, name, rows, dim, device=None):
+    """Row stride of a CUDA [rows, dim] matrix whose rows are contiguous."""
+    if t.dtype is not dtype or not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name}: expected a two-dimensional CUDA {dtype} tensor with contiguous rows, got "
                          f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-    if t.shape[1] != dim:
-        raise ValueError(f"{name}: rows of {t.shape[1]}, expected {dim}")
-    return t.stride(0) if t.shape[0] > 1 else max(dim, t.stride(0))
+    if t.shape != (rows, dim):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected ({rows}, {dim})")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    ld = t.stride(0)
+    return ld if rows > 1 or ld > dim else dim
 
 
 def _same_device(device, **tensors):
@@ -586,50 +609,62 @@ class MxAct:
         return self.buf[off:off + 4 * n].view(torch.bfloat16).view(2, self.desc.M_pad, self.r)
 
 
+def _check_quantize_mx(X, w, act):
+    if act.K != w.K or act.r != w.r:
+        raise ValueError(f"act (K={act.K} r={act.r}) does not match the weight (K={w.K} r={w.r})")
+    ldx = _rows(X, torch.bfloat16, "X", act.M, w.K, act.device)
+    if w.device != act.device:
+        raise ValueError(f"weight is on {w.device}, expected {act.device}")
+    return ("svdq_mx_quantize_act", X.data_ptr(), ldx, byref(w.desc), byref(act.desc))
+
+
 def quantize_act_mx(X: torch.Tensor, w: MxWeight, act: MxAct) -> MxAct:
     """Smoothing + MXFP4 quantization + low-rank down-projection in one pass over X [M, K] (rows of
     any 16-byte stride)."""
-    ldx = _rows(X, torch.bfloat16, "X", w.K)
-    if X.shape[0] != act.M:
-        raise ValueError("X shape does not match the act buffer / weight")
-    _same_device(X.device, weight=w, act=act)
-    with torch.cuda.device(X.device):
-        _check("svdq_mx_quantize_act", lib().svdq_mx_quantize_act(_ptr(X), ldx, byref(w.desc), byref(act.desc),
-                                                                  _stream(X.device)))
+    _enqueue(act.device, _check_quantize_mx(X, w, act))
     return act
+
+
+def _check_gemm_mx(act, w, bias, epilogue, out_dtype, out):
+    if epilogue is None:
+        epilogue = (EPI_BIAS if bias is not None else EPI_NONE) | (EPI_SWIGLU if w.swiglu else 0)
+    n_out = w.N // 2 if epilogue & EPI_SWIGLU else w.N
+    if out_dtype not in _OUT_CODES:
+        raise ValueError(f"out_dtype {out_dtype}: expected bfloat16 or float32")
+    device = act.device
+    if out is None:
+        out, ldy = torch.empty((act.M, n_out), dtype=out_dtype, device=device), n_out
+    else:
+        ldy = _rows(out, out_dtype, "out", act.M, n_out, device)
+    if bias is not None:
+        _need(bias, torch.bfloat16, "bias", 1)
+        if bias.shape[0] != w.N or bias.device != device:
+            raise ValueError(f"bias: [{bias.shape[0]}] on {bias.device}, expected [{w.N}] on {device}")
+    if w.device != device:
+        raise ValueError(f"weight is on {w.device}, expected {device}")
+    return out, ("svdq_mx_gemm", byref(act.desc), byref(w.desc), None if bias is None else bias.data_ptr(), epilogue,
+                 out.data_ptr(), ldy, _OUT_CODES[out_dtype])
+
+
+_OUT_CODES = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
 
 
 def gemm_mx(act: MxAct, w: MxWeight, bias: torch.Tensor | None = None, epilogue: int | None = None,
             out_dtype=torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
     """The MXFP4 GEMM + low-rank up-projection + bias / SwiGLU epilogue. `out` may have any row stride
     of whole 16-byte units."""
-    if epilogue is None:
-        epilogue = (EPI_BIAS if bias is not None else EPI_NONE) | (EPI_SWIGLU if w.swiglu else 0)
-    n_out = w.N // 2 if epilogue & EPI_SWIGLU else w.N
-    if out_dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"out_dtype {out_dtype}: expected bfloat16 or float32")
-    if out is None:
-        out = torch.empty(act.M, n_out, dtype=out_dtype, device=act.device)
-    ldy = _rows(out, out_dtype, "out", n_out)
-    if out.shape[0] != act.M:
-        raise ValueError(f"out: {out.shape[0]} rows, expected {act.M}")
-    if bias is not None:
-        _need(bias, torch.bfloat16, "bias", 1)
-        if bias.shape[0] != w.N:
-            raise ValueError("bias must be [N]")
-    _same_device(act.device, weight=w, bias=bias, out=out)
-    code = OUT_F32 if out_dtype == torch.float32 else OUT_BF16
-    with torch.cuda.device(act.device):
-        _check("svdq_mx_gemm", lib().svdq_mx_gemm(byref(act.desc), byref(w.desc), _ptr(bias), epilogue, _ptr(out),
-                                                  ldy, code, _stream(act.device)))
+    out, call = _check_gemm_mx(act, w, bias, epilogue, out_dtype, out)
+    _enqueue(act.device, call)
     return out
 
 
 def linear_mx(X, w: MxWeight, bias=None, act: MxAct | None = None, out=None, out_dtype=torch.bfloat16):
     """The whole MXFP4 layer on the current stream (the format has no tensor scale to calibrate)."""
     act = MxAct(X.shape[0], w.K, w.r, X.device) if act is None else act
-    quantize_act_mx(X, w, act)
-    return gemm_mx(act, w, bias, out=out, out_dtype=out_dtype)
+    quantize = _check_quantize_mx(X, w, act)
+    out, gemm_call = _check_gemm_mx(act, w, bias, None, out_dtype, out)
+    _enqueue(act.device, quantize, gemm_call)
+    return out
 
 
 def _export_mx(fn, obj, rows):
@@ -650,18 +685,13 @@ def export_act_mx(act: MxAct):
 
 def dequantize_act_mx(act: MxAct, out: torch.Tensor | None = None, out_dtype=torch.bfloat16) -> torch.Tensor:
     """The values the quantized (smoothed) activation stands for, [M, K]."""
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    if out_dtype not in _OUT_CODES:
         raise ValueError(f"out_dtype {out_dtype}: expected bfloat16 or float32")
     if out is None:
-        out = torch.empty(act.M, act.K, dtype=out_dtype, device=act.device)
-    ld = _rows(out, out_dtype, "out", act.K)
-    if out.shape[0] != act.M:
-        raise ValueError(f"out: {out.shape[0]} rows, expected {act.M}")
-    _same_device(act.device, out=out)
-    code = OUT_F32 if out_dtype == torch.float32 else OUT_BF16
-    with torch.cuda.device(act.device):
-        _check("svdq_mx_dequantize_act", lib().svdq_mx_dequantize_act(byref(act.desc), _ptr(out), ld, code,
-                                                                      _stream(act.device)))
+        out, ld = torch.empty((act.M, act.K), dtype=out_dtype, device=act.device), act.K
+    else:
+        ld = _rows(out, out_dtype, "out", act.M, act.K, act.device)
+    _enqueue(act.device, ("svdq_mx_dequantize_act", byref(act.desc), out.data_ptr(), ld, _OUT_CODES[out_dtype]))
     return out
 
 
@@ -695,84 +725,87 @@ class Norm:
             _same_device(self.device, weight=weight, bias=bias)
 
 
-_FLOATS = (torch.bfloat16, torch.float32)
+_F32 = {torch.bfloat16: 0, torch.float32: 1}
 
 
 def _norm_rows(t, name, shape=None, device=None):
     """(pointer, row stride, fp32 flag) of a [M, D] or [B, T, D] activation whose rows are evenly spaced."""
-    if t.dtype not in _FLOATS or not t.is_cuda or t.dim() not in (2, 3):
+    f32, sh = _F32.get(t.dtype), t.shape
+    if f32 is None or not t.is_cuda or len(sh) not in (2, 3):
         raise ValueError(f"{name}: expected a CUDA bf16 or fp32 tensor [rows, D] or [samples, rows, D], got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    st, sh = t.stride(), t.shape
-    D, T = sh[-1], sh[-2]
+                         f"{tuple(sh)} on {t.device}")
+    if shape is not None and (sh != shape or t.device != device):
+        raise ValueError(f"{name}: shape {tuple(sh)} on {t.device}, expected {tuple(shape)} on {device}")
+    D = sh[-1]
+    if t.is_contiguous():
+        return t.data_ptr(), D, f32
+    st, T = t.stride(), sh[-2]
     ld = st[-2] if T > 1 else (st[0] if len(sh) == 3 and sh[0] > 1 else D)
     if (D > 1 and st[-1] != 1) or (len(sh) == 3 and sh[0] > 1 and T > 1 and st[0] != T * ld):
         raise ValueError(f"{name}: rows must be contiguous and evenly spaced, got strides {st}")
-    if ld < D and t.numel() and t.shape[:-1].numel() > 1:
+    if ld < D and sh[:-1].numel() > 1:
         raise ValueError(f"{name}: rows overlap (strides {st})")
-    return t.data_ptr(), max(ld, D), t.dtype == torch.float32
+    return t.data_ptr(), max(ld, D), f32
+
+
+def _mod(m, name, D, samples, device, f32):
+    """(pointer, sample stride) of a gate, scale or shift [D] or [samples, D]."""
+    if m is None:
+        return None, 0
+    if _F32.get(m.dtype) != f32 or m.device != device:
+        raise ValueError("gate, scale and shift: expected tensors of one type, bf16 or fp32, on x's device")
+    sh = m.shape
+    if (sh != (D,) and sh != (samples, D) and sh != (1, D)) or (D > 1 and m.stride(-1) != 1):
+        raise ValueError(f"{name}: shape {tuple(sh)}, expected [D] or [samples, D] = [{samples}, {D}] with contiguous "
+                         "rows")
+    return m.data_ptr(), m.stride(0) if len(sh) == 2 and sh[0] > 1 else 0
+
+
+_NO_NORM = SvdqNorm()
 
 
 def _norm_args(x, y, gate, post, res_scale, skip_scale, norm, scale, shift, offsets, out, h):
-    a = SvdqBlockNormArgs()
     device, shape = x.device, x.shape
-    a.x, a.ldx, a.x_f32 = _norm_rows(x, "x")
+    px, ldx, x_f32 = _norm_rows(x, "x")
     D = shape[-1]
-    a.M, a.D = shape[:-1].numel(), D
     if offsets is not None:
         if len(shape) != 2:
             raise ValueError("x: expected [rows, D] with offsets")
         if offsets.dtype != torch.int32 or offsets.device != device or offsets.dim() != 1 or offsets.shape[0] < 2 \
                 or not offsets.is_contiguous():
             raise ValueError("offsets: expected a contiguous int32 [samples + 1] tensor on x's device")
-        a.samples, a.offsets = offsets.shape[0] - 1, offsets.data_ptr()
+        M, samples, T, p_off = shape[0], offsets.shape[0] - 1, 0, offsets.data_ptr()
     else:
-        a.samples, a.rows_per_sample = (shape[0], max(1, shape[1])) if len(shape) == 3 else (1, max(1, shape[0]))
-        a.samples = max(1, a.samples)
-    mods = [m for m in (gate, scale, shift) if m is not None]
-    if mods:
-        a.mod_f32 = mods[0].dtype == torch.float32
-    for name, m in (("gate", gate), ("scale", scale), ("shift", shift)):
-        if m is None:
-            continue
-        if m.dtype not in _FLOATS or m.dtype != mods[0].dtype or m.device != device:
-            raise ValueError("gate, scale and shift: expected tensors of one type, bf16 or fp32, on x's device")
-        if m.shape not in ((D,), (1, D), (a.samples, D)) or (D > 1 and m.stride(-1) != 1):
-            raise ValueError(f"{name}: shape {tuple(m.shape)}, expected [D] or [samples, D] = [{a.samples}, {D}] with "
-                             "contiguous rows")
-        setattr(a, name, m.data_ptr())
-        setattr(a, "ld_" + name, m.stride(0) if m.dim() == 2 and m.shape[0] > 1 else 0)
+        samples, T = (shape[0], shape[1]) if len(shape) == 3 else (1, shape[0])
+        M, samples, T, p_off = samples * T, samples or 1, T or 1, None
+    first = gate if gate is not None else scale if scale is not None else shift
+    mod_f32 = 0 if first is None else _F32.get(first.dtype, -1)
+    p_gate, ld_gate = _mod(gate, "gate", D, samples, device, mod_f32)
+    p_scale, ld_scale = _mod(scale, "scale", D, samples, device, mod_f32)
+    p_shift, ld_shift = _mod(shift, "shift", D, samples, device, mod_f32)
     for name, n in (("post", post), ("norm", norm)):
-        if n is not None:
-            if n.D is not None and (n.D != D or n.device != device):
-                raise ValueError(f"{name}: vectors of {n.D} on {n.device}, expected {D} on {device}")
-            setattr(a, name, n.desc)
+        if n is not None and n.D is not None and (n.D != D or n.device != device):
+            raise ValueError(f"{name}: vectors of {n.D} on {n.device}, expected {D} on {device}")
+    py, ldy, y_f32, po, ldo = None, 0, 0, None, 0
     if y is not None:
-        a.y, a.ldy, a.y_f32 = _norm_rows(y, "y", shape, device)
-        if out is not None:
-            a.x_out, a.ld_out, f32 = _norm_rows(out, "out", shape, device)
-            if f32 != a.x_f32:
-                raise ValueError(f"out: {out.dtype}, expected x's {x.dtype}")
-        a.skip_scale, a.res_scale = skip_scale, res_scale
-    if h is not None:
-        a.h, a.ldh, a.h_f32 = _norm_rows(h, "h", shape, device)
-    return a
+        py, ldy, y_f32 = _norm_rows(y, "y", shape, device)
+        po, ldo, o_f32 = _norm_rows(out, "out", shape, device)
+        if o_f32 != x_f32:
+            raise ValueError(f"out: {out.dtype}, expected x's {x.dtype}")
+    ph, ldh, h_f32 = (None, 0, 0) if h is None else _norm_rows(h, "h", shape, device)
+    return SvdqBlockNormArgs(M, D, samples, T, p_off, px, ldx, x_f32, y_f32, py, ldy, po, ldo, ph, ldh, h_f32, mod_f32,
+                             p_gate, ld_gate, p_scale, ld_scale, p_shift, ld_shift, skip_scale, res_scale,
+                             _NO_NORM if post is None else post.desc, _NO_NORM if norm is None else norm.desc)
 
 
 def _run_norm(a, device, w=None, act=None):
     if a.M == 0:
         return  # no row: empty tensors have no address to pass
-    with torch.cuda.device(device):
-        if act is None:
-            _check("svdq_block_norm", lib().svdq_block_norm(byref(a), _stream(device)))
-        else:
-            _same_device(device, weight=w, act=act)
-            _check("svdq_block_norm_quantize_mx", lib().svdq_block_norm_quantize_mx(
-                byref(a), byref(w.desc), byref(act.desc), _stream(device)))
+    if act is None:
+        _enqueue(device, ("svdq_block_norm", byref(a)))
+    else:
+        _same_device(device, weight=w, act=act)
+        _enqueue(device, ("svdq_block_norm_quantize_mx", byref(a), byref(w.desc), byref(act.desc)))
 
 
 def block_norm(x, norm: Norm, scale=None, shift=None, offsets=None, out=None, out_dtype=None):
@@ -780,7 +813,7 @@ def block_norm(x, norm: Norm, scale=None, shift=None, offsets=None, out=None, ou
     shift [D] or one row per sample. `offsets` (int32 [samples + 1]) gives packed samples of x [rows, D];
     rows outside them are left as they are in `out`. out_dtype defaults to x's (or out's) type."""
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)  # contiguous whatever x's strides
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out: {out.dtype}, expected {out_dtype}")
     _run_norm(_norm_args(x, None, None, None, 1.0, 1.0, norm, scale, shift, offsets, None, out), x.device)
