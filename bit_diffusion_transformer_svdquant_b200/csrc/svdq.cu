@@ -1882,7 +1882,7 @@ svdq_status svdq_mx_dequantize_act(const svdq_mx_act* act, void* out, long long 
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   set_programmatic(attr[0]);
-  cfg.gridDim = dim3(grid_for(static_cast<size_t>(act->M) * (act->K / 8), 256, sms), 1, 1);
+  cfg.gridDim = dim3((act->M + svdq::mx::kDeqRows - 1) / svdq::mx::kDeqRows, (act->K / 8 + 255) / 256, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;

@@ -17,6 +17,7 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "svdq_gemm.cuh"
 #include "svdq_ptx.cuh"
@@ -212,18 +213,18 @@ struct Gemm {
       }
     }
   }
-  // y = acc (+ bias); bias columns past N (padding of the last tile, clipped by the store) are not read
+  // y = acc (+ bias); columns past N (padding of the last tile, clipped by the store) take the last bias
+  // columns instead of reading past the end
   struct Epi {
     __device__ Epi(const Args&, int) {}
     template <bool BIAS, class V>
     __device__ void apply8(const Args& a, V& v, int off, int, const __nv_bfloat16* bias8) const {
       if constexpr (BIAS) {
-        if (bias8 - a.bias < a.N) {
-          float b[8];
-          bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(bias8)), b);
+        const __nv_bfloat16* last = a.bias + (a.N - 8);
+        float b[8];
+        bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(bias8 < last ? bias8 : last)), b);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[off + j] += b[j];
-        }
+        for (int j = 0; j < 8; ++j) v[off + j] += b[j];
       }
     }
   };
@@ -302,38 +303,48 @@ __global__ void export_kernel(const uint8_t* __restrict__ codes, const uint8_t* 
   }
 }
 
-// E2M1 code -> its value: sign, then magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-  const uint32_t m = c & 7u;
-  const float a = m < 2u ? 0.5f * static_cast<float>(m) : __uint_as_float((126u + (m >> 1)) << 23 | (m & 1u) << 22);
-  return c & 8u ? -a : a;
+// Two E2M1 codes (a byte, low nibble first) -> their values.
+__device__ __forceinline__ float2 e2m1x2_value(uint32_t byte) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(byte));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// The values of a quantized activation, one thread per 8: dec(q) 2^e, exact in fp32.
+// The values of a quantized activation: dec(q) 2^e, exact in fp32. A thread takes 8 columns of kDeqRows
+// rows, whose loads go out together; writing the values bounds it.
+constexpr int kDeqRows = 4;
 template <bool F32>
-__global__ void dequantize_act_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ sf, int M, int K,
-                                      int K_pad, void* __restrict__ out, long long ld) {
+__global__ void __launch_bounds__(256) dequantize_act_kernel(const uint8_t* __restrict__ codes,
+                                                             const uint8_t* __restrict__ sf, int M, int K, int K_pad,
+                                                             void* __restrict__ out, long long ld) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const int per_row = K >> 3;
-  const size_t total = static_cast<size_t>(M) * per_row;
-  for (size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x; i < total;
-       i += static_cast<size_t>(gridDim.x) * blockDim.x) {
-    const int m = static_cast<int>(i / per_row), c = static_cast<int>(i - static_cast<size_t>(m) * per_row);
-    const uint32_t q = *reinterpret_cast<const uint32_t*>(codes + static_cast<size_t>(m) * (K_pad >> 1) + 4 * c);
-    const float s = scale_value(sf[act_sf_offset(m, c >> 2, K_pad)]);
-    float v[8];
+  const int m0 = blockIdx.x * kDeqRows, c = blockIdx.y * 256 + threadIdx.x;
+  if (8 * c >= K) return;
+  uint32_t q[kDeqRows], e[kDeqRows];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = e2m1_value(q >> (4 * j)) * s;
+  for (int r = 0; r < kDeqRows; ++r) {
+    const int m = m0 + r;  // a row of padding (allocated up to M_pad) may be read
+    q[r] = __ldg(reinterpret_cast<const uint32_t*>(codes + static_cast<size_t>(m) * (K_pad >> 1) + 4 * c));
+    e[r] = __ldg(sf + act_sf_offset(m, c >> 2, K_pad));
+  }
+#pragma unroll
+  for (int r = 0; r < kDeqRows; ++r) {
+    const long long m = m0 + r;
+    if (m >= M) break;
+    const float s = scale_value(e[r]);
+    float2 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = mul2_rn(e2m1x2_value((q[r] >> (8 * j)) & 0xFFu), make_float2(s, s));
     if constexpr (F32) {
       float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + m * ld + 8 * c);
-      o[0] = make_float4(v[0], v[1], v[2], v[3]);
-      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+      o[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+      o[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
     } else {
       uint32_t w[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[j].x, v[j].y);
         w[j] = *reinterpret_cast<const uint32_t*>(&b2);
       }
       *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + m * ld + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
