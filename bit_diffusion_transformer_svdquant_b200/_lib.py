@@ -47,7 +47,7 @@ class SvdqFp8rAct(ctypes.Structure):
 class SvdqMxWeight(ctypes.Structure):
     _fields_ = [("N", c_int), ("K", c_int), ("r", c_int), ("swiglu_interleaved", c_int), ("n_tile", c_int),
                 ("N_pad", c_int), ("K_pad", c_int), ("reserved0", c_int), ("codes", c_void_p), ("scales", c_void_p),
-                ("inv_lambda", c_void_p), ("L1s_t", c_void_p), ("L2_t", c_void_p), ("tmap", c_ulonglong * 48)]
+                ("inv_lambda", c_void_p), ("L1s_t", c_void_p), ("L2_t", c_void_p), ("tmap", c_ulonglong * 80)]
 
 
 class SvdqMxAct(ctypes.Structure):

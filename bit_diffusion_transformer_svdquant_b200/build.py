@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(REPO, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libsvdq.so")
 SOURCES = [os.path.join(CSRC, "svdq.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("svdq_ptx.cuh", "svdq_quant.cuh", "svdq_gemm.cuh", "svdq_fp8r.cuh", "svdq_fused.cuh", "svdq_mx.cuh",
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("svdq_ptx.cuh", "svdq_quant.cuh", "svdq_gemm.cuh", "svdq_fp8r.cuh", "svdq_fused.cuh", "svdq_mx.cuh", "svdq_mx_few.cuh",
                                                     "svdq_norm.cuh")] + [
     os.path.join(INCLUDE, "svdq.h")]
 

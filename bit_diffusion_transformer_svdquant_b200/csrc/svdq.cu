@@ -17,6 +17,7 @@
 #include "svdq_fused.cuh"
 #include "svdq_gemm.cuh"
 #include "svdq_mx.cuh"
+#include "svdq_mx_few.cuh"
 #include "svdq_norm.cuh"
 #include "svdq_ptx.cuh"
 #include "svdq_quant.cuh"
@@ -1449,8 +1450,45 @@ using MxLayout = svdq::PairGemmLayout<true, N_TILE, STAGES, svdq::mx::Gemm::kSfA
 struct MxState {
   bool ready = false;
   int max_pairs[3] = {0, 0, 0};  // co-resident CTA pairs of the MXFP4 GEMM for n_tile 384, 256, 128
+  int few_clusters[4] = {0, 0, 0, 0};  // co-resident few-row clusters of 1, 2, 4 and 8 CTAs
 };
 MxState g_mx[64];
+
+// A few-row block asks for at least this much shared memory, so that an SM holds one: its TMEM columns
+// (up to 512) are then free when it starts, and no cluster can wait for columns that another waiting
+// cluster holds.
+constexpr int kFewMinSmem = 116 * 1024;
+constexpr int kFewMaxSmem = 226 * 1024;
+
+// The few-row quantizer holds its share of up to 8 raw rows in shared memory: 2 K bytes.
+constexpr int kFewQuantMaxK = 49152;
+template <int R>
+svdq_status mx_few_quant_setup() {
+  SVDQ_CUDA(cudaFuncSetAttribute(svdq::mx::few_quant_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 2 * kFewQuantMaxK));
+  return SVDQ_OK;
+}
+
+template <int NB>
+svdq_status mx_few_setup(int sms, int* clusters) {
+  auto* kern = svdq::mx::few_gemm_kernel<NB>;
+  SVDQ_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewMaxSmem));
+  for (int i = 0; i < 4; ++i) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1 << i;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((sms >> i) << i, 1, 1);
+    cfg.blockDim = dim3(svdq::mx::kFewThreads, 1, 1);
+    cfg.dynamicSmemBytes = kFewMinSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    SVDQ_CUDA(cudaOccupancyMaxActiveClusters(&clusters[i], kern, &cfg));
+  }
+  return SVDQ_OK;
+}
 
 template <int N_TILE, int STAGES>
 svdq_status mx_gemm_setup(int sms, int* max_pairs) {
@@ -1479,6 +1517,11 @@ svdq_status mx_ready(int* dev_out, int* sm_out) {
     if (s == SVDQ_OK) s = mx_quant_setup<16>();
     if (s == SVDQ_OK) s = mx_quant_setup<32>();
     if (s == SVDQ_OK) s = mx_quant_setup<64>();
+    if (s == SVDQ_OK) s = mx_few_quant_setup<16>();
+    if (s == SVDQ_OK) s = mx_few_quant_setup<32>();
+    if (s == SVDQ_OK) s = mx_few_quant_setup<64>();
+    if (s == SVDQ_OK) s = mx_few_setup<2>(sms, st.few_clusters);
+    if (s == SVDQ_OK) s = mx_few_setup<1>(sms, st.few_clusters);
     if (s != SVDQ_OK) return s;
     st.ready = true;
   }
@@ -1503,6 +1546,11 @@ int mx_n_tile(int N, int swiglu) {
 }
 int mx_n_pad(int N, int swiglu) {
   return swiglu ? round_up(N / 2, 128) * 2 : round_up(N, mx_n_tile(N, 0));
+}
+
+int mx_few_rows() {
+  if (const char* env = getenv("MX_FEW")) return atoi(env);
+  return svdq::mx::kFewRows;
 }
 
 struct MxWeightLayout {
@@ -1567,6 +1615,81 @@ svdq_status check_mx_act(const svdq_mx_act* a) {
   return SVDQ_OK;
 }
 
+// The few-row product; *done stays false where the pair GEMM is to run (no split of K that fits).
+svdq_status mx_few_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const uint16_t* bias, bool has_bias, bool swiglu,
+                        void* Y, long long ldy, int esize, int dev, svdq_stream_t stream, bool* done) {
+  const int NB = swiglu ? 2 : 1, r = w->r;
+  const int cols = act->M <= 16 ? 16 : act->M <= 32 ? 32 : 64;
+  const int blocks = w->N_pad / (128 * NB), steps = w->K_pad / 256;
+  int ranks_log = 0;
+  {
+    std::lock_guard<std::mutex> lk(g_dev_mu);
+    for (int i = 1; i < 4; ++i)
+      if (blocks <= g_mx[dev].few_clusters[i] && (1 << i) <= steps) ranks_log = i;
+  }
+  const int ranks = 1 << ranks_log;
+  const int stage = svdq::mx::few_stage_bytes(NB, cols);
+  const int part = svdq::mx::few_part_bytes(NB, cols);
+  const int slots = (steps + ranks - 1) / ranks + (r + 31) / 32;
+  int stages = (kFewMaxSmem - 1024 - part) / stage;
+  if (stages > slots) stages = slots;
+  if (stages > 12) stages = 12;
+  int tmem = 32;
+  while (tmem < NB * cols + stages * svdq::mx::few_stage_tmem(NB)) tmem *= 2;
+  if (stages < 1 || tmem > 512) return SVDQ_OK;
+  CUtensorMap tmW, tmX, tmU, tmL2;
+  std::memset(&tmU, 0, sizeof(tmU));
+  std::memcpy(&tmW, &w->tmap[3][0], sizeof(CUtensorMap));
+  std::memcpy(&tmL2, &w->tmap[4][0], sizeof(CUtensorMap));
+  if (svdq_status s = make_tmap(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, act->codes, act->K_pad / 2, act->M_pad,
+                                act->K_pad / 2, 128, cols, CU_TENSOR_MAP_SWIZZLE_128B);
+      s != SVDQ_OK)
+    return s;
+  if (r > 0) {
+    if (svdq_status s = make_tmap(&tmU, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, act->U, r, 2 * static_cast<uint64_t>(act->M_pad),
+                                  static_cast<uint64_t>(r) * 2, r < 32 ? r : 32, cols, lr_swizzle(r));
+        s != SVDQ_OK)
+      return s;
+  }
+  svdq::mx::FewGemmArgs g{};
+  g.sfw = static_cast<const uint8_t*>(w->scales);
+  g.sfx = static_cast<const uint8_t*>(act->scales);
+  g.bias = reinterpret_cast<const __nv_bfloat16*>(bias);
+  g.Y = Y;
+  g.ldy = ldy;
+  g.wait_ns = g_wait_ns.load();
+  g.M = act->M;
+  g.M_pad = act->M_pad;
+  g.N = w->N;
+  g.K = w->K_pad;
+  g.r = r;
+  g.n_tile = w->n_tile;
+  g.cols = cols;
+  g.stages = stages;
+  g.tmem_cols = tmem;
+  g.out_f32 = esize == 4 ? 1 : 0;
+  g.has_bias = has_bias ? 1 : 0;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  set_programmatic(attr[1]);
+  cfg.gridDim = dim3(blocks * ranks, 1, 1);
+  cfg.blockDim = dim3(svdq::mx::kFewThreads, 1, 1);
+  const int smem = stages * stage + part + 1024;
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem < kFewMinSmem ? kFewMinSmem : smem);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, NB == 2 ? svdq::mx::few_gemm_kernel<2> : svdq::mx::few_gemm_kernel<1>,
+                                           tmW, tmX, tmU, tmL2, g);
+  if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, "launch of mx::few_gemm_kernel failed: %s", cudaGetErrorString(e));
+  *done = true;
+  return check_launch("mx::few_gemm_kernel");
+}
+
 svdq_status mx_fill_weight(uint8_t* b, int N, int K, int r, int swiglu, svdq_mx_weight* out) {
   svdq_mx_weight w{};
   w.N = N;
@@ -1582,15 +1705,25 @@ svdq_status mx_fill_weight(uint8_t* b, int N, int K, int r, int swiglu, svdq_mx_
   w.inv_lambda = reinterpret_cast<float*>(b + l.inv_lambda);
   w.L1s_t = b + l.l1t;
   w.L2_t = b + l.l2t;
-  static_assert(sizeof(w.tmap) >= 3 * sizeof(CUtensorMap), "tmap storage");
-  CUtensorMap tmB, tmL2, tmL1;
+  static_assert(sizeof(w.tmap) >= 5 * sizeof(CUtensorMap), "tmap storage");
+  CUtensorMap tmB, tmL2, tmL1, tmB64, tmL264;
+  std::memset(&tmL264, 0, sizeof(tmL264));
   std::memset(&tmL2, 0, sizeof(tmL2));
   std::memset(&tmL1, 0, sizeof(tmL1));
   if (svdq_status s = make_tmap(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, w.K_pad / 2, w.N_pad, w.K_pad / 2, 128,
                                 w.n_tile / 2, CU_TENSOR_MAP_SWIZZLE_128B);
       s != SVDQ_OK)
     return s;
+  // the same in boxes of 64 rows: the few-row product's blocks of 128 tile columns
+  if (svdq_status s = make_tmap(&tmB64, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, w.K_pad / 2, w.N_pad, w.K_pad / 2, 128, 64,
+                                CU_TENSOR_MAP_SWIZZLE_128B);
+      s != SVDQ_OK)
+    return s;
   if (r > 0) {
+    if (svdq_status s = make_tmap(&tmL264, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, w.L2_t, r, w.N_pad,
+                                  static_cast<uint64_t>(r) * 2, r < 32 ? r : 32, 64, lr_swizzle(r));
+        s != SVDQ_OK)
+      return s;
     if (svdq_status s = make_tmap(&tmL2, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, w.L2_t, r, w.N_pad,
                                   static_cast<uint64_t>(r) * 2, r < 32 ? r : 32, w.n_tile / 2, lr_swizzle(r));
         s != SVDQ_OK)
@@ -1603,6 +1736,8 @@ svdq_status mx_fill_weight(uint8_t* b, int N, int K, int r, int swiglu, svdq_mx_
   std::memcpy(&w.tmap[0][0], &tmB, sizeof(CUtensorMap));
   std::memcpy(&w.tmap[1][0], &tmL2, sizeof(CUtensorMap));
   std::memcpy(&w.tmap[2][0], &tmL1, sizeof(CUtensorMap));
+  std::memcpy(&w.tmap[3][0], &tmB64, sizeof(CUtensorMap));
+  std::memcpy(&w.tmap[4][0], &tmL264, sizeof(CUtensorMap));
   *out = w;
   return SVDQ_OK;
 }
@@ -1702,6 +1837,43 @@ svdq_status svdq_mx_quantize_act(const uint16_t* X, long long ldx, const svdq_mx
   int dev, sms;
   if (svdq_status s = mx_ready(&dev, &sms); s != SVDQ_OK) return s;
   const int r = w->r;
+  if (act->M <= mx_few_rows() && (r == 0 || act->K_pad <= kFewQuantMaxK)) {
+    svdq::mx::FewQuantArgs f{};
+    f.X = reinterpret_cast<const __nv_bfloat16*>(X);
+    f.ldx = ldx;
+    f.inv_lambda = w->inv_lambda;
+    f.L1s_t = static_cast<const __nv_bfloat16*>(w->L1s_t);
+    f.codes = static_cast<uint8_t*>(act->codes);
+    f.sf = static_cast<uint8_t*>(act->scales);
+    f.U = static_cast<__nv_bfloat16*>(act->U);
+    f.M = act->M;
+    f.K = act->K;
+    f.K_pad = act->K_pad;
+    f.M_pad = act->M_pad;
+    f.rows = act->M >= 8 ? 8 : act->M >= 3 ? 4 : act->M;
+    const int x_smem = r > 0 ? f.rows * (act->K_pad / svdq::mx::kFewQuantCluster) * 2 : 0;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = svdq::mx::kFewQuantCluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    set_programmatic(attr[1]);
+    cfg.gridDim = dim3((act->M + f.rows - 1) / f.rows * svdq::mx::kFewQuantCluster, 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(x_smem);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg,
+                                             r == 0    ? svdq::mx::few_quant_kernel<0>
+                                             : r == 16 ? svdq::mx::few_quant_kernel<16>
+                                             : r == 32 ? svdq::mx::few_quant_kernel<32>
+                                                       : svdq::mx::few_quant_kernel<64>,
+                                             f);
+    if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, "launch of mx::few_quant_kernel failed: %s", cudaGetErrorString(e));
+    return check_launch("mx::few_quant_kernel");
+  }
   CUtensorMap tmX, tmL1;
   std::memcpy(&tmL1, &w->tmap[2][0], sizeof(CUtensorMap));
   if (svdq_status s = make_tmap(&tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, X, act->K, act->M,
@@ -1783,6 +1955,11 @@ svdq_status svdq_mx_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const 
   int dev, sms;
   if (svdq_status s = mx_ready(&dev, &sms); s != SVDQ_OK) return s;
 
+  if (act->M <= mx_few_rows()) {
+    bool done = false;
+    if (svdq_status s = mx_few_gemm(act, w, bias, has_bias, swiglu, Y, ldy, esize, dev, stream, &done); s != SVDQ_OK || done)
+      return s;
+  }
   const int r = w->r, n_tile = w->n_tile;
   CUtensorMap tmA, tmU, tmB, tmL2, tmY;
   std::memset(&tmU, 0, sizeof(tmU));

@@ -324,13 +324,13 @@ typedef struct svdq_mx_weight {
   float* inv_lambda;      /* device fp32 [K_pad] smoothing reciprocals (1 in the padding)        */
   void* L1s_t;            /* bf16 [r][K_pad] = (diag(lambda)^-1 L1)^T                            */
   void* L2_t;             /* bf16 [N_pad][r] = L2^T, rows in GEMM order                          */
-  unsigned long long tmap[3][16]; /* opaque: cached TMA descriptors of codes, L2_t and L1s_t     */
+  unsigned long long tmap[5][16]; /* opaque: cached TMA descriptors of codes, L2_t and L1s_t     */
 } svdq_mx_weight;
 
 typedef struct svdq_mx_act {
   int M, K, r, M_pad, K_pad; /* M_pad = M up to a multiple of 128                                */
   int reserved0;
-  void* codes;            /* uint8 [M_pad][K_pad/2] E2M1 codes (zero in the padding)             */
+  void* codes;            /* uint8 [M_pad][K_pad/2] E2M1 codes (zero past K; rows >= M undefined)*/
   void* scales;           /* E8M0, [M_pad/128][K_pad/128] atoms of 512 bytes: byte               */
                           /*   (m%32)*16 + ((m%128)/32)*4 + (k/32)%4 of atom (m/128, k/128)      */
   void* U;                /* bf16 [2][M_pad][r]: u = fp32(X L1s) as hi = bf16(u), lo = bf16(u - hi) */

@@ -266,9 +266,9 @@ def test_quantized_is_the_unfused_chain(cuda_device, B, T, D):
     for a, b in ((act, want), (pre, pre_want)):
         for u, v in zip(svdq.export_act_mx(a), svdq.export_act_mx(b)):
             assert torch.equal(u, v)
-        # padding too: the product reads whole tiles
+        # the padding past K too: the product reads whole K steps
         assert torch.equal(svdq.gemm_mx(a, w), svdq.gemm_mx(b, w))
-        n = a.desc.M_pad * a.desc.K_pad // 2
+        n = a.M * a.desc.K_pad // 2
         assert torch.equal(a.buf[:n], b.buf[:n])
 
 
