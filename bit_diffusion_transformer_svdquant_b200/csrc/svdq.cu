@@ -1548,9 +1548,17 @@ int mx_n_pad(int N, int swiglu) {
   return swiglu ? round_up(N / 2, 128) * 2 : round_up(N, mx_n_tile(N, 0));
 }
 
-int mx_few_rows() {
-  if (const char* env = getenv("MX_FEW")) return atoi(env);
-  return svdq::mx::kFewRows;
+// Where the few-row kernels run (measured on B200 with weights from HBM; quantizer, product in us).
+// The quantizer up to 128 rows: at K = 3072, r = 32 it takes 4.0 (one row) to 7.1 (128) against kernel 1's
+// 11.2, at K = 12288 7.8 to 18.8 against 27.3, at K = 256 3.9 to 4.2 against 5.4.
+// The product up to 48 rows, and up to 128 where K covers the wider epilogue: 3072 -> 9216 9.9 against the
+// pair GEMM's 11.3 at 40 rows, 11.6 / 11.8 at 96, 12.7 / 12.0 at 128; 12288 -> 3072 11.1 / 27.0 at one
+// row, 14.1 / 27.8 at 128; 256 -> 9216 5.2 / 5.6 at 40, 6.2 / 5.8 at 64, 8.9 / 6.2 at 128.
+bool mx_few_quant_rows(int M, int K_pad, int r) {
+  return M <= svdq::mx::kFewRows && (r == 0 || K_pad <= kFewQuantMaxK);
+}
+bool mx_few_product_rows(int M, int K_pad) {
+  return M <= 48 || (M <= svdq::mx::kFewRows && K_pad >= 32 * M);
 }
 
 struct MxWeightLayout {
@@ -1619,7 +1627,7 @@ svdq_status check_mx_act(const svdq_mx_act* a) {
 svdq_status mx_few_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const uint16_t* bias, bool has_bias, bool swiglu,
                         void* Y, long long ldy, int esize, int dev, svdq_stream_t stream, bool* done) {
   const int NB = swiglu ? 2 : 1, r = w->r;
-  const int cols = act->M <= 16 ? 16 : act->M <= 32 ? 32 : 64;
+  const int cols = act->M <= 16 ? 16 : act->M <= 32 ? 32 : act->M <= 64 ? 64 : 128;
   const int blocks = w->N_pad / (128 * NB), steps = w->K_pad / 256;
   int ranks_log = 0;
   {
@@ -1636,7 +1644,7 @@ svdq_status mx_few_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const u
   if (stages > 12) stages = 12;
   int tmem = 32;
   while (tmem < NB * cols + stages * svdq::mx::few_stage_tmem(NB)) tmem *= 2;
-  if (stages < 1 || tmem > 512) return SVDQ_OK;
+  if (stages < 2 || tmem > 512) return SVDQ_OK;
   CUtensorMap tmW, tmX, tmU, tmL2;
   std::memset(&tmU, 0, sizeof(tmU));
   std::memcpy(&tmW, &w->tmap[3][0], sizeof(CUtensorMap));
@@ -1837,7 +1845,7 @@ svdq_status svdq_mx_quantize_act(const uint16_t* X, long long ldx, const svdq_mx
   int dev, sms;
   if (svdq_status s = mx_ready(&dev, &sms); s != SVDQ_OK) return s;
   const int r = w->r;
-  if (act->M <= mx_few_rows() && (r == 0 || act->K_pad <= kFewQuantMaxK)) {
+  if (mx_few_quant_rows(act->M, act->K_pad, r)) {
     svdq::mx::FewQuantArgs f{};
     f.X = reinterpret_cast<const __nv_bfloat16*>(X);
     f.ldx = ldx;
@@ -1850,7 +1858,10 @@ svdq_status svdq_mx_quantize_act(const uint16_t* X, long long ldx, const svdq_mx
     f.K = act->K;
     f.K_pad = act->K_pad;
     f.M_pad = act->M_pad;
-    f.rows = act->M >= 8 ? 8 : act->M >= 3 ? 4 : act->M;
+    // rows per cluster: the fewest that keep all clusters on the SMs at once (K = 12288, r = 32: one row
+    // per cluster 7.8 us, eight 15.8 us)
+    f.rows = 1;
+    while (f.rows < 8 && (act->M + f.rows - 1) / f.rows * svdq::mx::kFewQuantCluster > sms) f.rows *= 2;
     const int x_smem = r > 0 ? f.rows * (act->K_pad / svdq::mx::kFewQuantCluster) * 2 : 0;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[2];
@@ -1955,7 +1966,7 @@ svdq_status svdq_mx_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const 
   int dev, sms;
   if (svdq_status s = mx_ready(&dev, &sms); s != SVDQ_OK) return s;
 
-  if (act->M <= mx_few_rows()) {
+  if (mx_few_product_rows(act->M, act->K_pad)) {
     bool done = false;
     if (svdq_status s = mx_few_gemm(act, w, bias, has_bias, swiglu, Y, ldy, esize, dev, stream, &done); s != SVDQ_OK || done)
       return s;

@@ -1,8 +1,8 @@
-// The MXFP4 layer for few rows (single tokens, conditioning vectors, short batches): up to 64.
+// The MXFP4 layer for few rows (single tokens, conditioning vectors, short batches): up to 128.
 //
 // At few rows the layer streams its weight: 17/32 bytes per weight element, read once. The pair GEMM's 256-row
 // tiles then leave most of the tensor pipe and, at 24 to 72 tiles, most SMs idle, so here the roles are
-// exchanged: 128 weight rows are the MMA's M side, the tokens its N side (16, 32 or 64 columns), and K is
+// exchanged: 128 weight rows are the MMA's M side, the tokens its N side (16 to 128 columns), and K is
 // split over a thread-block cluster, so that about every SM streams a share of the weight. Each CTA sums
 // its K share in TMEM; the partial sums meet in distributed shared memory, every CTA of the cluster
 // finishing its part of the tokens, in rank order (the result does not depend on timing).
@@ -22,7 +22,7 @@
 namespace svdq {
 namespace mx {
 
-constexpr int kFewRows = 64;
+constexpr int kFewRows = 128;
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -206,7 +206,7 @@ struct FewGemmArgs {
   long long ldy;
   unsigned long long wait_ns;
   int M, M_pad, N, K, r;      // N: the weight's true width, K: padded
-  int n_tile, cols;           // cols: token columns of the MMA (16, 32 or 64)
+  int n_tile, cols;           // cols: token columns of the MMA (16, 32, 64 or 128)
   int stages, tmem_cols, out_f32, has_bias;
 };
 constexpr int kFewThreads = 192;  // warp 0: TMA, warp 1: TMEM and MMA, warps 2..5: epilogue

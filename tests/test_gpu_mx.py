@@ -225,3 +225,17 @@ def test_headline_layer_sampled(cuda_device):
     err = np.abs(y[rows.to(cuda_device)].cpu().double().numpy() - mxfp4.layer_forward(X, prep, wq, bias))
     assert np.all(err <= _bound(X, prep, xq, wq, bias, False))
     assert svdq.device_status() == 0
+
+
+@pytest.mark.parametrize("M", [1, 2, 5, 16, 19, 37, 48, 49, 73, 96, 128])
+@pytest.mark.parametrize("K,N,r,swiglu", [(3072, 640, 32, False), (1032, 768, 64, True), (4096, 1152, 16, False),
+                                          (6144, 128, 0, False)])
+def test_few_rows(cuda_device, M, K, N, r, swiglu):
+    """Row counts on both sides of every split of the few-row kernels: rows per cluster, token columns, K
+    shares of one to eight CTAs, 384-, 256- and 128-wide tiles, both halves of a SwiGLU tile."""
+    _check(*_layer(M, K, N, r, M * 3 + K, M % 2 == 1), swiglu, cuda_device)
+
+
+def test_few_rows_of_a_wide_layer(cuda_device):
+    """More blocks of output columns than SMs, and a stage ring that wraps."""
+    _check(*_layer(3, 6400, 19200, 32, 77, True), False, cuda_device)
