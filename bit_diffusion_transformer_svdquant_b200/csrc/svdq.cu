@@ -1549,16 +1549,18 @@ int mx_n_pad(int N, int swiglu) {
 }
 
 // Where the few-row kernels run (measured on B200 with weights from HBM; quantizer, product in us).
-// The quantizer up to 128 rows: at K = 3072, r = 32 it takes 4.0 (one row) to 7.1 (128) against kernel 1's
-// 11.2, at K = 12288 7.8 to 18.8 against 27.3, at K = 256 3.9 to 4.2 against 5.4.
+// The quantizer up to 384 rows with a branch (every group of 8 rows reads L1s^T again), up to 1024 without:
+// K = 3072, r = 32: 4.2 (one row) to 8.6 (384) against kernel 1's 11.1, 14.9 / 11.1 at 512; K = 12288, r = 32:
+// 8.1 to 24.1 against 27.2, 41 / 27 at 512; K = 1024, r = 32: 5.6 / 7.0 at 384; K = 3072, r = 0: 1.5 to 4.3 against
+// 6.4, 7.2 / 6.6 at 2048; K = 1024, r = 0: 3.0 / 3.6 at 1024, 3.9 / 3.6 at 1536.
 // The product up to 48 rows, and up to 128 where K covers the wider epilogue: 3072 -> 9216 9.9 against the
 // pair GEMM's 11.3 at 40 rows, 11.6 / 11.8 at 96, 12.7 / 12.0 at 128; 12288 -> 3072 11.1 / 27.0 at one
 // row, 14.1 / 27.8 at 128; 256 -> 9216 5.2 / 5.6 at 40, 6.2 / 5.8 at 64, 8.9 / 6.2 at 128.
 bool mx_few_quant_rows(int M, int K_pad, int r) {
-  return M <= svdq::mx::kFewRows && (r == 0 || K_pad <= kFewQuantMaxK);
+  return r == 0 ? M <= 1024 : M <= 384 && K_pad <= kFewQuantMaxK;
 }
 bool mx_few_product_rows(int M, int K_pad) {
-  return M <= 48 || (M <= svdq::mx::kFewRows && K_pad >= 32 * M);
+  return M <= 48 || (M <= svdq::mx::kFewCols && K_pad >= 32 * M);
 }
 
 struct MxWeightLayout {

@@ -1,4 +1,4 @@
-// The MXFP4 layer for few rows (single tokens, conditioning vectors, short batches): up to 128.
+// The MXFP4 layer for few rows (single tokens, conditioning vectors, short batches).
 //
 // At few rows the layer streams its weight: 17/32 bytes per weight element, read once. The pair GEMM's 256-row
 // tiles then leave most of the tensor pipe and, at 24 to 72 tiles, most SMs idle, so here the roles are
@@ -22,7 +22,7 @@
 namespace svdq {
 namespace mx {
 
-constexpr int kFewRows = 128;
+constexpr int kFewCols = 128;  // the product's tokens at most
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
