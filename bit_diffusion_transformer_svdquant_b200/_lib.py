@@ -8,6 +8,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 from ctypes import POINTER, byref, c_char_p, c_float, c_int, c_longlong, c_size_t, c_ulonglong, c_void_p
 
 import torch
@@ -82,7 +83,7 @@ _lib = None
 def _declare(lib):
     W, A = POINTER(SvdqWeight), POINTER(SvdqAct)
     FW, FA = POINTER(SvdqFp8rWeight), POINTER(SvdqFp8rAct)
-    MW, MA, BN = POINTER(SvdqMxWeight), POINTER(SvdqMxAct), POINTER(SvdqBlockNormArgs)
+    MW, MA = POINTER(SvdqMxWeight), POINTER(SvdqMxAct)
     sig = {
         "svdq_fp8r_weight_bytes": (c_size_t, [c_int, c_int, c_int]),
         "svdq_fp8r_act_bytes": (c_size_t, [c_int, c_int, c_int]),
@@ -104,8 +105,8 @@ def _declare(lib):
         "svdq_mx_export_weight": (c_int, [MW, c_void_p, c_void_p, c_void_p]),
         "svdq_mx_export_act": (c_int, [MA, c_void_p, c_void_p, c_void_p]),
         "svdq_mx_dequantize_act": (c_int, [MA, c_void_p, c_longlong, c_int, c_void_p]),
-        "svdq_block_norm": (c_int, [BN, c_void_p]),
-        "svdq_block_norm_quantize_mx": (c_int, [BN, MW, MA, c_void_p]),
+        "svdq_block_norm": (c_int, [c_void_p, c_void_p]),
+        "svdq_block_norm_quantize_mx": (c_int, [c_void_p, MW, MA, c_void_p]),
         "svdq_mlp_scratch_bytes": (c_size_t, [c_int, c_int]),
         "svdq_gemm_swiglu_quant": (c_int, [A, W, c_void_p, W, c_void_p, A, c_void_p, c_size_t, c_void_p, c_void_p]),
         "svdq_gemm_swiglu_quant_noscratch": (c_int, [A, W, c_void_p, W, c_void_p, A, c_void_p, c_void_p]),
@@ -633,7 +634,7 @@ def _check_gemm_mx(act, w, bias, epilogue, out_dtype, out):
         raise ValueError(f"out_dtype {out_dtype}: expected bfloat16 or float32")
     device = act.device
     if out is None:
-        out, ldy = torch.empty((act.M, n_out), dtype=out_dtype, device=device), n_out
+        out, ldy = act.buf.new_empty((act.M, n_out), dtype=out_dtype), n_out
     else:
         ldy = _rows(out, out_dtype, "out", act.M, n_out, device)
     if bias is not None:
@@ -688,7 +689,7 @@ def dequantize_act_mx(act: MxAct, out: torch.Tensor | None = None, out_dtype=tor
     if out_dtype not in _OUT_CODES:
         raise ValueError(f"out_dtype {out_dtype}: expected bfloat16 or float32")
     if out is None:
-        out, ld = torch.empty((act.M, act.K), dtype=out_dtype, device=act.device), act.K
+        out, ld = act.buf.new_empty((act.M, act.K), dtype=out_dtype), act.K
     else:
         ld = _rows(out, out_dtype, "out", act.M, act.K, act.device)
     _enqueue(act.device, ("svdq_mx_dequantize_act", byref(act.desc), out.data_ptr(), ld, _OUT_CODES[out_dtype]))
@@ -717,12 +718,12 @@ class Norm:
             if v.dtype not in (torch.bfloat16, torch.float32) or not v.is_cuda or v.dim() != 1 \
                     or not v.is_contiguous() or v.dtype != given[0].dtype or v.shape != given[0].shape:
                 raise ValueError("weight and bias: expected contiguous CUDA [D] tensors of one type, bf16 or fp32")
-        self.desc = SvdqNorm(kind=NORM_KINDS[kind], eps=self.eps)
         if given:
             self.D, self.device = given[0].shape[0], given[0].device
-            self.desc.f32 = given[0].dtype == torch.float32
-            self.desc.weight, self.desc.bias = _ptr(weight), _ptr(bias)
             _same_device(self.device, weight=weight, bias=bias)
+        # the fields of svdq_norm
+        self.fields = (NORM_KINDS[kind], self.eps, int(bool(given) and given[0].dtype == torch.float32), 0,
+                       0 if weight is None else weight.data_ptr(), 0 if bias is None else bias.data_ptr())
 
 
 _F32 = {torch.bfloat16: 0, torch.float32: 1}
@@ -751,7 +752,7 @@ def _norm_rows(t, name, shape=None, device=None):
 def _mod(m, name, D, samples, device, f32):
     """(pointer, sample stride) of a gate, scale or shift [D] or [samples, D]."""
     if m is None:
-        return None, 0
+        return 0, 0
     if _F32.get(m.dtype) != f32 or m.device != device:
         raise ValueError("gate, scale and shift: expected tensors of one type, bf16 or fp32, on x's device")
     sh = m.shape
@@ -761,7 +762,9 @@ def _mod(m, name, D, samples, device, f32):
     return m.data_ptr(), m.stride(0) if len(sh) == 2 and sh[0] > 1 else 0
 
 
-_NO_NORM = SvdqNorm()
+_NO_NORM = (0, 0.0, 0, 0, 0, 0)
+# svdq_block_norm_args field by field, as SvdqBlockNormArgs: packing takes a fifth of filling that structure
+_PACK_NORM_ARGS = struct.Struct("@4iPPqiiPqPqPqiiPqPqPqff" + 2 * "ifiiPP").pack
 
 
 def _norm_args(x, y, gate, post, res_scale, skip_scale, norm, scale, shift, offsets, out, h):
@@ -777,7 +780,7 @@ def _norm_args(x, y, gate, post, res_scale, skip_scale, norm, scale, shift, offs
         M, samples, T, p_off = shape[0], offsets.shape[0] - 1, 0, offsets.data_ptr()
     else:
         samples, T = (shape[0], shape[1]) if len(shape) == 3 else (1, shape[0])
-        M, samples, T, p_off = samples * T, samples or 1, T or 1, None
+        M, samples, T, p_off = samples * T, samples or 1, T or 1, 0
     first = gate if gate is not None else scale if scale is not None else shift
     mod_f32 = 0 if first is None else _F32.get(first.dtype, -1)
     p_gate, ld_gate = _mod(gate, "gate", D, samples, device, mod_f32)
@@ -786,26 +789,35 @@ def _norm_args(x, y, gate, post, res_scale, skip_scale, norm, scale, shift, offs
     for name, n in (("post", post), ("norm", norm)):
         if n is not None and n.D is not None and (n.D != D or n.device != device):
             raise ValueError(f"{name}: vectors of {n.D} on {n.device}, expected {D} on {device}")
-    py, ldy, y_f32, po, ldo = None, 0, 0, None, 0
+    py, ldy, y_f32, po, ldo = 0, 0, 0, 0, 0
     if y is not None:
         py, ldy, y_f32 = _norm_rows(y, "y", shape, device)
         po, ldo, o_f32 = _norm_rows(out, "out", shape, device)
         if o_f32 != x_f32:
             raise ValueError(f"out: {out.dtype}, expected x's {x.dtype}")
-    ph, ldh, h_f32 = (None, 0, 0) if h is None else _norm_rows(h, "h", shape, device)
-    return SvdqBlockNormArgs(M, D, samples, T, p_off, px, ldx, x_f32, y_f32, py, ldy, po, ldo, ph, ldh, h_f32, mod_f32,
-                             p_gate, ld_gate, p_scale, ld_scale, p_shift, ld_shift, skip_scale, res_scale,
-                             _NO_NORM if post is None else post.desc, _NO_NORM if norm is None else norm.desc)
+    ph, ldh, h_f32 = (0, 0, 0) if h is None else _norm_rows(h, "h", shape, device)
+    if M == 0:
+        return None  # no row: empty tensors have no address to pass
+    return _PACK_NORM_ARGS(M, D, samples, T, p_off, px, ldx, x_f32, y_f32, py, ldy, po, ldo, ph, ldh, h_f32, mod_f32,
+                           p_gate, ld_gate, p_scale, ld_scale, p_shift, ld_shift, skip_scale, res_scale,
+                           *(_NO_NORM if post is None else post.fields), *(_NO_NORM if norm is None else norm.fields))
 
 
 def _run_norm(a, device, w=None, act=None):
-    if a.M == 0:
-        return  # no row: empty tensors have no address to pass
+    if a is None:
+        return
     if act is None:
-        _enqueue(device, ("svdq_block_norm", byref(a)))
+        _enqueue(device, ("svdq_block_norm", a))
     else:
         _same_device(device, weight=w, act=act)
-        _enqueue(device, ("svdq_block_norm_quantize_mx", byref(a), byref(w.desc), byref(act.desc)))
+        _enqueue(device, ("svdq_block_norm_quantize_mx", a, byref(w.desc), byref(act.desc)))
+
+
+def _like(x, dtype):
+    """A contiguous tensor of x's shape."""
+    if dtype is None or dtype is x.dtype:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
 
 
 def block_norm(x, norm: Norm, scale=None, shift=None, offsets=None, out=None, out_dtype=None):
@@ -813,7 +825,7 @@ def block_norm(x, norm: Norm, scale=None, shift=None, offsets=None, out=None, ou
     shift [D] or one row per sample. `offsets` (int32 [samples + 1]) gives packed samples of x [rows, D];
     rows outside them are left as they are in `out`. out_dtype defaults to x's (or out's) type."""
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)  # contiguous whatever x's strides
+        out = _like(x, out_dtype)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out: {out.dtype}, expected {out_dtype}")
     _run_norm(_norm_args(x, None, None, None, 1.0, 1.0, norm, scale, shift, offsets, None, out), x.device)
@@ -825,11 +837,11 @@ def gated_residual(x, y, gate=None, post: Norm | None = None, res_scale: float =
     """A block's end, x' = skip_scale x + res_scale gate post(y), and (with `norm`) the next block's
     norm h = norm(x') (1 + scale) + shift, in one pass. Returns x', or (x', h). `out` may be x itself
     (the residual stream updated in place). h_dtype defaults to y's type."""
-    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    out = _like(x, None) if out is None else out
     if norm is None and (h is not None or h_dtype is not None):
         raise ValueError("h without a norm")
     if norm is not None and h is None:
-        h = torch.empty(x.shape, dtype=h_dtype or y.dtype, device=x.device)
+        h = _like(x, h_dtype or y.dtype)
     elif h is not None and h_dtype is not None and h.dtype != h_dtype:
         raise ValueError(f"h: {h.dtype}, expected {h_dtype}")
     _run_norm(_norm_args(x, y, gate, post, res_scale, skip_scale, norm, scale, shift, offsets, out, h), x.device)
@@ -848,7 +860,7 @@ def gated_residual_quantize_mx(x, y, norm: Norm, w: MxWeight, act: MxAct, gate=N
                                out=None):
     """gated_residual with norm whose bf16 h is quantized for the next layer instead of stored. Returns
     (x', act). For weights without a branch."""
-    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    out = _like(x, None) if out is None else out
     _run_norm(_norm_args(x, y, gate, post, res_scale, skip_scale, norm, scale, shift, offsets, out, None), x.device, w,
               act)
     return out, act

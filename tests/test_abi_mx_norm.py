@@ -266,3 +266,19 @@ def test_struct_layouts_match_c(tmp_path):
     B = _lib.SvdqBlockNormArgs
     assert got == [ctypes.sizeof(_lib.SvdqMxWeight), ctypes.sizeof(_lib.SvdqMxAct), ctypes.sizeof(_lib.SvdqNorm),
                    ctypes.sizeof(B), _lib.SvdqMxWeight.tmap.offset, B.post.offset, B.shift.offset]
+
+
+def test_packed_norm_arguments_are_the_structure():
+    """The binding packs svdq_block_norm_args as bytes: every field lands where the structure has it."""
+    B = _lib.SvdqBlockNormArgs
+    flat = []
+    for name, ctype in B._fields_:
+        flat += [f"{name}.{n}" for n, _ in ctype._fields_] if ctype is _lib.SvdqNorm else [name]
+    packed = _lib._PACK_NORM_ARGS(*range(1, len(flat) + 1))
+    assert len(packed) == ctypes.sizeof(B)
+    a = B.from_buffer_copy(packed)
+    for value, name in enumerate(flat, 1):
+        obj = a
+        for part in name.split("."):
+            obj = getattr(obj, part)
+        assert obj == value, name
