@@ -866,6 +866,41 @@ def gated_residual_quantize_mx(x, y, norm: Norm, w: MxWeight, act: MxAct, gate=N
     return out, act
 
 
+def mlp_mx(x, w_up: MxWeight, w_down: MxWeight, bias_up=None, bias_down=None, norm: Norm | None = None, scale=None,
+           shift=None, post: Norm | None = None, gate=None, res_scale: float = 1.0, skip_scale: float = 1.0, offsets=None,
+           acts: tuple[MxAct, MxAct] | None = None, out=None):
+    """The MXFP4 MLP chain, x -> SwiGLU(x W_up^T + b_up) -> (.) W_down^T + b_down (x [rows, K] bf16; result
+    bf16). With `norm` it is a transformer's whole MLP block on the residual stream x ([rows, K] or
+    [samples, rows, K], bf16 or fp32):
+        skip_scale x + res_scale gate post(mlp(norm(x) (1 + scale) + shift))
+    in x's type, with samples, `offsets` and `out` as in gated_residual. The norm's result is quantized
+    where it is computed if w_up has no branch. acts: the activation buffers of the two layers, for
+    callers that keep them."""
+    if not w_up.swiglu or w_down.K != w_up.N // 2:
+        raise ValueError(f"w_up must be packed with swiglu=True and w_down take its {w_up.N // 2} outputs, not {w_down.K}")
+    if norm is None:
+        if any(v is not None for v in (scale, shift, post, gate, offsets)):
+            raise ValueError("scale, shift, post, gate and offsets belong to the block form: give its norm")
+    elif w_down.N != x.shape[-1]:
+        raise ValueError(f"w_down returns {w_down.N} values to a residual stream of {x.shape[-1]}")
+    rows = x.shape[:-1].numel()
+    if rows == 0:
+        return _like(x, None) if norm is not None else x.new_empty((0, w_down.N))
+    act_up, act_down = acts or (MxAct(rows, w_up.K, w_up.r, x.device), MxAct(rows, w_down.K, w_down.r, x.device))
+    if norm is None:
+        quantize_act_mx(x, w_up, act_up)
+    elif w_up.r == 0:
+        norm_quantize_act_mx(x, norm, w_up, act_up, scale, shift, offsets)
+    else:
+        h = block_norm(x, norm, scale, shift, offsets, out_dtype=torch.bfloat16)
+        quantize_act_mx(h.view(rows, w_up.K), w_up, act_up)
+    y = linear_mx(gemm_mx(act_up, w_up, bias_up), w_down, bias_down, act_down, out=out if norm is None else None)
+    if norm is None:
+        return y
+    return gated_residual(x, y.view(x.shape), gate=gate, post=post, res_scale=res_scale, skip_scale=skip_scale,
+                          offsets=offsets, out=out)
+
+
 def device_status(reset: bool = True) -> int:
     """Synchronizes; returns 0, or the SVDQ_ERR_TIMEOUT status if a bounded device wait ran out."""
     return lib().svdq_device_status(1 if reset else 0)

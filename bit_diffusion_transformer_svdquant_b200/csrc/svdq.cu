@@ -2295,11 +2295,12 @@ svdq_status run_norm(const svdq_block_norm_args* a, const svdq_mx_weight* w, con
   if (vec) {
     const auto stage_bytes = [&] { return norm_batch(chunks) * chunks * 256 * W * elem_bytes; };
     const auto factor_bytes = [&] { return chunks * 256 * W * (a->y ? 12 : 8); };
+    const auto lambda_bytes = [&] { return act ? chunks * 256 * W * 4 : 0; };
     // factors of a run's sample in shared memory where a run gives every group two batches; else (or
     // where they do not fit beside a batch) two or eight chunks per thread and vectors read per row
     const int per_run = a->offsets ? a->M / a->samples : a->rows_per_sample;
     const bool share = per_run >= 2 * (svdq::norm::kMaxWarps / W) * norm_batch(chunks) &&
-                       stage_bytes() + factor_bytes() <= kNormSmem;
+                       stage_bytes() + factor_bytes() + lambda_bytes() <= kNormSmem;
     if (!share) {
       W = row_warps(2);
       chunks = (eights + 32 * W - 1) / (32 * W) <= 2 ? 2 : 8;
@@ -2310,12 +2311,16 @@ svdq_status run_norm(const svdq_block_norm_args* a, const svdq_mx_weight* w, con
       // 3072, all bf16 (12 KB of x and y): 6 groups 137 us, 8 groups 157 us, 4 groups 171 us, 6 groups with
       // two stages 138 us; without y (6 KB) over 4608 rows: 8 groups 13.2 us, 6 groups 15.2 us, 8 groups with
       // two stages 13.9 us; 4000 rows of 8192 without y (2 groups, 32 KB): one stage 33.8 us, two 32.1 us.
-      constexpr int kInFlight = 80 * 1024;
-      const int sets = 2 * factor_bytes() + stage_bytes() <= kNormSmem ? 2 : 1;
-      const int fixed = share ? sets * factor_bytes() : 0, R = norm_batch(chunks);
-      int groups = svdq::norm::kMaxWarps / W;
-      while (groups > 1 && (groups * stage_bytes() > kInFlight || groups * stage_bytes() + fixed > kNormSmem)) --groups;
-      const int stages = 2 * groups * stage_bytes() <= kInFlight ? 2 : 1;
+      // A quantized output is bound by its instructions: more groups, up to 128 KB (16896 rows of 3072 with
+      // y: 6 groups 91 us, 8 groups 79 us).
+      // Two sets of factors where they cost no group.
+      const int in_flight = (act ? 128 : 80) * 1024, R = norm_batch(chunks);
+      int groups = svdq::norm::kMaxWarps / W, fixed = share ? factor_bytes() + lambda_bytes() : 0;
+      while (groups > 1 && (groups * stage_bytes() > in_flight || groups * stage_bytes() + fixed > kNormSmem)) --groups;
+      const int sets = share && groups * stage_bytes() + fixed + factor_bytes() <= kNormSmem ? 2 : 1;
+      if (sets == 2) fixed += factor_bytes();
+      const int stages =
+          2 * groups * stage_bytes() <= 80 * 1024 && 2 * groups * stage_bytes() + fixed <= kNormSmem ? 2 : 1;
       const int batches = (k.rows + R - 1) / R, blocks = (batches + groups - 1) / groups;
       cfg.gridDim = dim3(blocks < sms ? blocks : sms, 1, 1);
       cfg.blockDim = dim3(groups * 32 * W, 1, 1);

@@ -40,15 +40,13 @@ __device__ __forceinline__ float max3_nan_abs(float a, float b, float c) {
   asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// E8M0 code of a block whose largest magnitude is `amax`, and the factor 2^-e its elements take (0 for
-// code 255, whose codes are then forced to zero)
+// E8M0 code of a block whose largest magnitude is `amax` (sign clear), and the factor 2^-e its elements
+// take (an infinity for code 255, whose codes are then forced to zero)
 __device__ __forceinline__ uint32_t scale_code(float amax) {
-  const uint32_t f = (__float_as_uint(amax) >> 23) & 0xFFu;
-  return f == 255u ? 255u : (f > 2u ? f - 2u : 0u);
+  const int f = static_cast<int>(__float_as_uint(amax) >> 23);
+  return f == 255 ? 255u : static_cast<uint32_t>(max(f - 2, 0));
 }
-__device__ __forceinline__ float scale_inverse(uint32_t code) {
-  return code == 255u ? 0.0f : __uint_as_float((254u - code) << 23);
-}
+__device__ __forceinline__ float scale_inverse(uint32_t code) { return __uint_as_float((254u - code) << 23); }
 // 2^(code - 127); code 255 is NaN, code 0 the subnormal 2^-127
 __device__ __forceinline__ float scale_value(uint32_t code) {
   return code == 255u ? __uint_as_float(0x7FC00000u) : code == 0u ? __uint_as_float(0x00400000u)
@@ -72,16 +70,20 @@ __host__ __device__ __forceinline__ size_t wgt_sf_offset(int p, int kb, int K, i
 
 // One thread's 8 consecutive values; four adjacent lanes hold one block (all 32 lanes call together).
 // Returns the 8 packed codes and sets s to the block's scale code.
-__device__ __forceinline__ uint32_t quarter_block(const float (&v)[8], uint32_t& s) {
-  const float m0 = max3_nan_abs(v[0], v[1], v[2]), m1 = max3_nan_abs(v[3], v[4], v[5]);
-  float a = max_nan_abs(max3_nan_abs(m0, m1, v[6]), v[7]);
+__device__ __forceinline__ uint32_t quarter_block(const float2 (&v)[4], uint32_t& s) {
+  const float m0 = max3_nan_abs(v[0].x, v[0].y, v[1].x), m1 = max3_nan_abs(v[1].y, v[2].x, v[2].y);
+  float a = max_nan_abs(max3_nan_abs(m0, m1, v[3].x), v[3].y);
   a = max_nan_abs(a, __shfl_xor_sync(0xffffffffu, a, 1));
   a = max_nan_abs(a, __shfl_xor_sync(0xffffffffu, a, 2));
   s = scale_code(a);
   const float f = scale_inverse(s);
   float q[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(v[i], f);
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = mul2_rn(v[i], make_float2(f, f));
+    q[2 * i] = p.x;
+    q[2 * i + 1] = p.y;
+  }
   const uint32_t codes = cvt_e2m1x8(q);
   return s == 255u ? 0u : codes;
 }
@@ -242,12 +244,14 @@ __global__ void pack_quant_kernel(const float* __restrict__ R, int N, int K, int
        i += static_cast<size_t>(gridDim.x) * blockDim.x) {
     const int n = static_cast<int>(i / per_row);
     const int k = static_cast<int>(i - static_cast<size_t>(n) * per_row) * 8;
-    float v[8] = {};
+    float2 v[4] = {};
     if (k < K) {
       const float4* src = reinterpret_cast<const float4*>(R + static_cast<size_t>(n) * K + k);
       const float4 a0 = __ldg(src), a1 = __ldg(src + 1);
-      v[0] = a0.x; v[1] = a0.y; v[2] = a0.z; v[3] = a0.w;
-      v[4] = a1.x; v[5] = a1.y; v[6] = a1.z; v[7] = a1.w;
+      v[0] = make_float2(a0.x, a0.y);
+      v[1] = make_float2(a0.z, a0.w);
+      v[2] = make_float2(a1.x, a1.y);
+      v[3] = make_float2(a1.z, a1.w);
     }
     uint32_t s;
     const uint32_t q = quarter_block(v, s);

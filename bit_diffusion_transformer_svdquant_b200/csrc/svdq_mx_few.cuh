@@ -90,16 +90,17 @@ __global__ void __launch_bounds__(256) few_quant_kernel(const FewQuantArgs a) {
       const bool in = c < eights;
       uint4 x = make_uint4(0u, 0u, 0u, 0u);
       if (in && k < a.K) x = ldg_stream(a.X + m * a.ldx + k);
-      float v[8], q[8];
+      float v[8];
       bf16x8_to_f32(x, v);
       float4 l0 = make_float4(1.0f, 1.0f, 1.0f, 1.0f), l1v = l0;
       if (in) {
         l0 = __ldg(reinterpret_cast<const float4*>(a.inv_lambda + k));
         l1v = __ldg(reinterpret_cast<const float4*>(a.inv_lambda + k + 4));
       }
-      const float l[8] = {l0.x, l0.y, l0.z, l0.w, l1v.x, l1v.y, l1v.z, l1v.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) q[e] = __fmul_rn(v[e], l[e]);
+      const float2 q[4] = {mul2_rn(make_float2(v[0], v[1]), make_float2(l0.x, l0.y)),
+                           mul2_rn(make_float2(v[2], v[3]), make_float2(l0.z, l0.w)),
+                           mul2_rn(make_float2(v[4], v[5]), make_float2(l1v.x, l1v.y)),
+                           mul2_rn(make_float2(v[6], v[7]), make_float2(l1v.z, l1v.w))};
       uint32_t s;
       const uint32_t codes = quarter_block(q, s);
       if (in) {

@@ -483,6 +483,18 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
     q[0] = make_float4(v[0], v[1], v[2], v[3]);
     q[G] = make_float4(v[4], v[5], v[6], v[7]);
   };
+  // the smoothing reciprocals of a quantized output: SHARE laid out like a factor behind the factor sets
+  float* const lambdas = factors + factor_sets * (has_y ? 3 : 2) * span;
+  auto smooth = [&](int c) -> F8 {
+    if constexpr (SHARE) {
+      const float4* q = reinterpret_cast<const float4*>(lambdas) + 2 * c * G + t;
+      return join(q[0], q[G]);
+    } else {
+      float l[8];
+      vec8<true>(l, Vec{a.inv_lambda, 0, 1}, 0, c, D, G, t);
+      return pair8(l);
+    }
+  };
   const float inv_d = 1.0f / static_cast<float>(D);
   const int chunks = (D - 8 * t + 8 * G - 1) / (8 * G);  // of this thread that hold elements of the row
   const long long out_step = a.ld_out * xs, h_step = a.ldh * (a.h_f32 ? 4 : 2);
@@ -516,6 +528,13 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
   };
 
   for (int i = 0; i < stages; ++i) fetch(i);
+  if constexpr (QUANT && SHARE) {
+    for (int c = group; c < C; c += groups) {
+      float l[8];
+      vec8<true>(l, Vec{a.inv_lambda, 0, 1}, 0, c, D, G, t);
+      put_factor(lambdas, 0, c, l);
+    }
+  }
   int built = 0, seen = 0;  // runs of samples: with factors in shared memory, entered
   if constexpr (SHARE) {
     // the first factor_sets runs' factors at once: most blocks have no more, and entering a run then
@@ -689,6 +708,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
 #pragma unroll
       for (int r = 0; r < R; ++r) rstd[r] = root(rstd[r], inv_d, a.pre.eps);
       uint8_t* const h_row = static_cast<uint8_t*>(a.h) + m * h_step;
+      const long long code_step = a.K_pad >> 1;
+      uint8_t* const code_row = a.codes + m * code_step;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int i = index<true>(c, 0, G, t);
@@ -712,23 +733,19 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
           if constexpr (QUANT) {
             // the codes svdq_mx_quantize_act makes of bf16(h): smoothing in fp32, blocks of four lanes
             F8 q = bf16x8(pack8_bf16(v[r][c]));
-            if (on) {
-              const float4 l0 = __ldg(reinterpret_cast<const float4*>(a.inv_lambda + i));
-              const float4 l1 = __ldg(reinterpret_cast<const float4*>(a.inv_lambda + i + 4));
-              q.p[0] = mul2_rn(q.p[0], make_float2(l0.x, l0.y));
-              q.p[1] = mul2_rn(q.p[1], make_float2(l0.z, l0.w));
-              q.p[2] = mul2_rn(q.p[2], make_float2(l1.x, l1.y));
-              q.p[3] = mul2_rn(q.p[3], make_float2(l1.z, l1.w));
-            } else {
+            const F8 l = smooth(c);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) q.p[j] = dup2(0.0f);  // NaN in a row's padding too
-            }
-            const float q8[8] = {q.p[0].x, q.p[0].y, q.p[1].x, q.p[1].y, q.p[2].x, q.p[2].y, q.p[3].x, q.p[3].y};
+            for (int j = 0; j < 4; ++j) q.p[j] = mul2_rn(q.p[j], l.p[j]);  // past D: 0, or NaN in a row of NaN
             uint32_t sc;
-            const uint32_t codes = mx::quarter_block(q8, sc);
+            const uint32_t codes = mx::quarter_block(q.p, sc);
+            // the scales of four blocks (16 lanes) go out as one word
+            sc <<= 2 * (lane & 12);
+            sc |= __shfl_xor_sync(0xffffffffu, sc, 4);
+            sc |= __shfl_xor_sync(0xffffffffu, sc, 8);
             if (i < a.K_pad && (R == 1 || m + r < run.end)) {
-              *reinterpret_cast<uint32_t*>(a.codes + static_cast<size_t>(m + r) * (a.K_pad >> 1) + (i >> 1)) = codes;
-              if ((i & 31) == 0) a.sf[mx::act_sf_offset(m + r, i >> 5, a.K_pad)] = static_cast<uint8_t>(sc);
+              *reinterpret_cast<uint32_t*>(code_row + r * code_step + (i >> 1)) = codes;
+              if ((lane & 15) == 0)
+                *reinterpret_cast<uint32_t*>(a.sf + mx::act_sf_offset(m + r, 0, a.K_pad) + ((i >> 7) << 9)) = sc;
             }
           }
         }

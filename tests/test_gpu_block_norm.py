@@ -332,3 +332,40 @@ def test_block_as_it_is_used(cuda_device):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(buf, want) and svdq.device_status() == 0
+
+
+@pytest.mark.parametrize("r", [0, 16])
+@pytest.mark.parametrize("xt", [BF16, F32])
+@pytest.mark.parametrize("packed", [False, True])
+def test_mlp_block_is_its_steps(cuda_device, r, xt, packed):
+    """mlp_mx with a norm: bit for bit the calls it stands for, with and without a branch, samples in a
+    batch or packed (rows behind the last sample stay as they were)."""
+    g = torch.Generator(device="cuda").manual_seed(r + 2)
+    B, T, D, F = 3, 50, 256, 384
+    rows = B * T + (5 if packed else 0)
+    x = _rand(g, rows, D, dtype=xt)
+    x = x if packed else x.view(B, T, D)
+    offsets = torch.tensor([0, 30, 30, B * T], dtype=torch.int32, device="cuda") if packed else None
+    gate, scale, shift = _rand(g, B, 3 * D, std=0.5).split(D, dim=1)
+    norm, post = _norm(g, "layer", D, False), _norm(g, "rms", D, True)
+
+    def weight(N, K, swiglu):
+        return svdq.MxWeight(_rand(g, N, K, dtype=F32, std=K ** -0.5), _rand(g, K, r, std=K ** -0.5) if r else None,
+                             _rand(g, r, N, std=0.1) if r else None, swiglu=swiglu)
+    up, down, b_up, b_down = weight(2 * F, D, True), weight(D, F, False), _rand(g, 2 * F), _rand(g, D)
+    out = torch.full_like(x, 7.0)
+    got = svdq.mlp_mx(x, up, down, b_up, b_down, norm, scale, shift, post, gate, 0.5, offsets=offsets, out=out)
+    h = torch.zeros(x.shape, dtype=BF16, device="cuda")
+    svdq.block_norm(x, norm, scale, shift, offsets, out=h)
+    y = svdq.mlp_mx(h.view(rows, D), up, down, b_up, b_down)
+    assert torch.equal(y, svdq.linear_mx(svdq.linear_mx(h.view(rows, D), up, b_up), down, b_down))
+    want = torch.full_like(x, 7.0)
+    svdq.gated_residual(x, y.view(x.shape), gate=gate, post=post, res_scale=0.5, offsets=offsets, out=want)
+    assert got.data_ptr() == out.data_ptr() and torch.equal(got, want)
+    if packed:
+        assert (got[B * T:] == 7.0).all()
+    assert svdq.mlp_mx(x[:0], up, down, norm=norm).shape == x[:0].shape
+    with pytest.raises(ValueError, match="block form"):
+        svdq.mlp_mx(h.view(rows, D), up, down, gate=gate)
+    with pytest.raises(ValueError, match="swiglu"):
+        svdq.mlp_mx(x, down, up, norm=norm)
