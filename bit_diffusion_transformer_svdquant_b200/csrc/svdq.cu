@@ -1536,13 +1536,12 @@ bool mx_n_ok(int N, int swiglu) { return N > 0 && N % (swiglu ? 16 : 8) == 0 && 
 int mx_k_pad(int K) { return (K + 255) / 256 * 256; }
 int round_up(int x, int to) { return (x + to - 1) / to * to; }
 
-// GEMM tile width along N: the widest whose padding adds no 128-column block; SwiGLU pairs gate and up
-// columns inside a tile of 256.
+// Tile width a weight is packed for: 384, which streams the fewest operand bytes per flop, unless padding N
+// to it costs more than that gains over 256 (large M on B200, GEMM us at 256 / 384: 16896x3072x9216 211 / 197,
+// 4608x12288x3072 62.5 / 57.0). SwiGLU pairs gate and up columns inside a tile of 256.
 int mx_n_tile(int N, int swiglu) {
   if (swiglu) return 256;
-  const int least = round_up(N, 128);
-  if (least % 384 == 0) return 384;
-  return least % 256 == 0 ? 256 : 128;
+  return round_up(N, 384) * 100ll <= round_up(N, 256) * 105ll ? 384 : 256;
 }
 int mx_n_pad(int N, int swiglu) {
   return swiglu ? round_up(N / 2, 128) * 2 : round_up(N, mx_n_tile(N, 0));
@@ -1630,7 +1629,7 @@ svdq_status mx_few_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const u
                         void* Y, long long ldy, int esize, int dev, svdq_stream_t stream, bool* done) {
   const int NB = swiglu ? 2 : 1, r = w->r;
   const int cols = act->M <= 16 ? 16 : act->M <= 32 ? 32 : act->M <= 64 ? 64 : 128;
-  const int blocks = w->N_pad / (128 * NB), steps = w->K_pad / 256;
+  const int blocks = swiglu ? w->N_pad / 256 : (w->N + 127) / 128, steps = w->K_pad / 256;
   int ranks_log = 0;
   {
     std::lock_guard<std::mutex> lk(g_dev_mu);
@@ -2007,23 +2006,33 @@ svdq_status svdq_mx_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const 
   g.r = r;
   g.m_tiles = act->M_pad / 128;
   g.m_pairs = (g.m_tiles + 1) / 2;
-  g.n_tiles = w->N_pad / n_tile;
   g.k_iters = w->K_pad / 256;
-  g.num_tiles = g.m_pairs * g.n_tiles;
   g.out_f32 = esize == 4 ? 1 : 0;
   g.epi = static_cast<int>(epi);
-  int max_pairs = 0;
+  g.n_tile = n_tile;
+  // 128-wide tiles where all of them run at once: more SMs share the work of a small layer (us at 128 / the
+  // packed width: 512x3072x3072 8.8 / 11.3, 1024x1024x768 5.2 / 7.5; with two rounds of them, 300x3072x9216,
+  // 14.7 / 12.3). SwiGLU's column pairs need the packed tile.
+  int tile = n_tile, max_pairs = 0;
   {
     std::lock_guard<std::mutex> lk(g_dev_mu);
-    max_pairs = g_mx[dev].max_pairs[n_tile == 384 ? 0 : n_tile == 256 ? 1 : 2];
+    const int* most = g_mx[dev].max_pairs;
+    if (!swiglu && static_cast<long long>(g.m_pairs) * ((w->N + 127) / 128) <= most[2]) tile = 128;
+    max_pairs = most[tile == 384 ? 0 : tile == 256 ? 1 : 2];
+  }
+  g.n_tiles = swiglu ? w->N_pad / 256 : (w->N + tile - 1) / tile;
+  g.num_tiles = g.m_pairs * g.n_tiles;
+  if (tile != n_tile) {  // boxes of 64 rows
+    std::memcpy(&tmB, &w->tmap[3][0], sizeof(CUtensorMap));
+    std::memcpy(&tmL2, &w->tmap[4][0], sizeof(CUtensorMap));
   }
   const int pairs = g.num_tiles < max_pairs ? g.num_tiles : max_pairs;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (n_tile == 384)
+  if (tile == 384)
     e = launch_pair_gemm(svdq::pair_gemm_kernel<svdq::mx::Gemm, 384, kMxStages384>, 2 * pairs,
                          MxLayout<384, kMxStages384>::kSmem, st, tmA, tmB, tmU, tmL2, tmY, g);
-  else if (n_tile == 256)
+  else if (tile == 256)
     e = launch_pair_gemm(svdq::pair_gemm_kernel<svdq::mx::Gemm, 256, kMxStages256>, 2 * pairs,
                          MxLayout<256, kMxStages256>::kSmem, st, tmA, tmB, tmU, tmL2, tmY, g);
   else

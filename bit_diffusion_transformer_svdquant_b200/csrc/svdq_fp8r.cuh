@@ -230,6 +230,10 @@ struct Fp8Gemm {
   using Args = GemmArgs;
   static constexpr bool kScales = false;
   static constexpr int kSfAtomsK = 4;  // of no effect without scale factors
+  template <int N_TILE>
+  __device__ static int b_row(const Args&, int n_blk, int rank) {
+    return n_blk * N_TILE + rank * (N_TILE / 2);
+  }
   static constexpr bool kL2HiLo = true;
   // the four MMAs of a 128-element K step (each K = 32, 32 bytes of codes per row)
   template <int N_TILE, int SF_ATOMS_B>

@@ -149,6 +149,19 @@ struct Nvfp4Gemm {
   static constexpr bool kScales = true;
   static constexpr int kSfAtomsK = 4;
   static constexpr bool kL2HiLo = false;
+  // first row of B that CTA `rank` of the pair stages for tile n_blk
+  template <int N_TILE>
+  __device__ static int b_row(const Args&, int n_blk, int rank) {
+    return n_blk * N_TILE + rank * (N_TILE / 2);
+  }
+  // the B scale atoms of K step kt (contiguous: the weight is packed per N_TILE)
+  template <int N_TILE, int BYTES>
+  __device__ static void load_sfb(const Args& a, int n_blk, int sf_row_stride, int kt, uint32_t dst, uint32_t bar) {
+    constexpr int kAtoms = (N_TILE + 127) / 128;
+    bulk_load(dst,
+              a.sfb + ((static_cast<size_t>(n_blk) * sf_row_stride + static_cast<size_t>(kt) * kSfAtomsK) * kAtoms << 9),
+              BYTES, bar);
+  }
   // the MMAs of a 256-element K step: four of K = 64 (32 bytes of codes per row); the SFA of MMA j
   // at tsf + 4j, its SFB atoms (128 tile columns each) from tsf + 16 + 4 SF_ATOMS_B j on
   template <int N_TILE, int SF_ATOMS_B>
@@ -302,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         int m_pair, n_blk;
         tile_coords(tile, args.m_pairs, args.n_tiles, m_pair, n_blk);
         const int m_blk = 2 * m_pair + static_cast<int>(rank);
-        const int b_row = n_blk * N_TILE + static_cast<int>(rank) * L::kBRows;
+        const int b_row = F::template b_row<N_TILE>(args, n_blk, static_cast<int>(rank));
         for (int c0 = 0; c0 < r; c0 += kLrChunk) {
           if (!(ok = mbar_wait_bounded(empty_bar(stage), phase ^ 1u, wait_ns, status, kStatusProducer, abort_flag)))
             break;
@@ -328,11 +341,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           const uint32_t sa = sbase + stage * L::kStage;
           if constexpr (F::kScales) {
             const uint8_t* sfa_tile = args.sfa + (static_cast<size_t>(m_sf) * sf_row_stride << 9);
-            const uint8_t* sfb_tile = args.sfb + (static_cast<size_t>(n_blk) * sf_row_stride * L::kSfAtomsB << 9);
             mbar_arrive_expect_tx(sf_land_bar(stage), L::kSfa + L::kSfb);
             bulk_load(sa + L::kOffSfa, sfa_tile + (static_cast<size_t>(kt) * kSfK << 9), L::kSfa, sf_land_bar(stage));
-            bulk_load(sa + L::kOffSfb, sfb_tile + (static_cast<size_t>(kt) * kSfK * L::kSfAtomsB << 9), L::kSfb,
-                      sf_land_bar(stage));
+            F::template load_sfb<N_TILE, L::kSfb>(args, n_blk, sf_row_stride, kt, sa + L::kOffSfb, sf_land_bar(stage));
           } else {
             (void)m_sf;
             (void)sf_row_stride;

@@ -188,6 +188,7 @@ struct GemmArgs {
   int M, M_pad, N, K, r;  // N: the weight's true width (the bias length), K: padded
   int m_tiles, m_pairs, n_tiles, k_iters, num_tiles;
   int out_f32, epi;       // epi bit 0: bias, bit 1: SwiGLU
+  int n_tile;             // the packed tile width; the kernel's own is this or 128
 };
 
 // The MXFP4 format of the pair GEMM. A K step's two scale atoms each serve two MMAs (data ids 0 and 2).
@@ -196,6 +197,32 @@ struct Gemm {
   static constexpr bool kScales = true;
   static constexpr int kSfAtomsK = 2;
   static constexpr bool kL2HiLo = false;
+  // The 128-wide kernel also takes a weight packed 256 or 384 wide: a block of 128 tile columns is two runs
+  // of 64 packed rows, one for each CTA of the pair, and one scale atom per 128 of K.
+  template <int N_TILE>
+  __device__ static int b_row(const Args& a, int n_blk, int rank) {
+    if constexpr (N_TILE == 128) {
+      const int per = a.n_tile >> 7, tile = n_blk / per;
+      return tile * a.n_tile + packed_of_tile_col((n_blk - tile * per) * 128 + 64 * rank, a.n_tile);
+    } else {
+      return n_blk * N_TILE + rank * (N_TILE / 2);
+    }
+  }
+  template <int N_TILE, int BYTES>
+  __device__ static void load_sfb(const Args& a, int n_blk, int sf_row_stride, int kt, uint32_t dst, uint32_t bar) {
+    if constexpr (N_TILE == 128) {
+      const int per = a.n_tile >> 7, tile = n_blk / per, at = n_blk - tile * per;
+#pragma unroll
+      for (int i = 0; i < kSfAtomsK; ++i)
+        bulk_load(dst + 512 * i,
+                  a.sfb + (((static_cast<size_t>(tile) * sf_row_stride + kt * kSfAtomsK + i) * per + at) << 9), 512, bar);
+    } else {
+      bulk_load(dst,
+                a.sfb + ((static_cast<size_t>(n_blk) * sf_row_stride + static_cast<size_t>(kt) * kSfAtomsK) *
+                             (N_TILE / 128) << 9),
+                BYTES, bar);
+    }
+  }
   template <int N_TILE, int SF_ATOMS_B>
   __device__ static void kstep(uint32_t d, uint32_t la, uint32_t lb, uint32_t hi_ab, uint32_t tsf,
                                uint32_t accumulate) {

@@ -316,7 +316,7 @@ SVDQ_API svdq_status svdq_gemm_swiglu_quant_noscratch(const svdq_act* act, const
 typedef struct svdq_mx_weight {
   int N, K, r;
   int swiglu_interleaved; /* 1: gate/up rows interleaved per n_tile (256)                       */
-  int n_tile;             /* GEMM tile width along N: 384, 256 or 128                           */
+  int n_tile;             /* GEMM tile width along N it is packed for: 384 or 256               */
   int N_pad, K_pad;
   int reserved0;
   void* codes;            /* uint8 [N_pad][K_pad/2] E2M1 codes, rows in GEMM order               */

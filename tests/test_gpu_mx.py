@@ -239,3 +239,10 @@ def test_few_rows(cuda_device, M, K, N, r, swiglu):
 def test_few_rows_of_a_wide_layer(cuda_device):
     """More blocks of output columns than SMs, and a stage ring that wraps."""
     _check(*_layer(3, 6400, 19200, 32, 77, True), False, cuda_device)
+
+
+@pytest.mark.parametrize("M,K,N,r", [(300, 512, 1536, 32), (513, 256, 2344, 64), (130, 1032, 392, 16), (700, 768, 640, 0)])
+def test_128_wide_tiles_of_a_wider_packing(cuda_device, M, K, N, r):
+    """Few enough blocks for 128-wide tiles, on weights packed 384 and 256 wide whose last tile is partly
+    padding."""
+    _check(*_layer(M, K, N, r, M + 5 * N, True), False, cuda_device)
