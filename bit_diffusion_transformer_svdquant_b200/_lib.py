@@ -68,7 +68,7 @@ class SvdqBlockNormArgs(ctypes.Structure):
                 ("ldh", c_longlong), ("h_f32", c_int), ("mod_f32", c_int), ("gate", c_void_p),
                 ("ld_gate", c_longlong), ("scale", c_void_p), ("ld_scale", c_longlong), ("shift", c_void_p),
                 ("ld_shift", c_longlong), ("skip_scale", c_float), ("res_scale", c_float), ("post", SvdqNorm),
-                ("norm", SvdqNorm)]
+                ("norm", SvdqNorm), ("sx", c_longlong), ("sy", c_longlong), ("s_out", c_longlong), ("sh", c_longlong)]
 
 
 class SvdqError(RuntimeError):
@@ -730,7 +730,7 @@ _F32 = {torch.bfloat16: 0, torch.float32: 1}
 
 
 def _norm_rows(t, name, shape=None, device=None):
-    """(pointer, row stride, fp32 flag) of a [M, D] or [B, T, D] activation whose rows are evenly spaced."""
+    """(pointer, row stride, fp32 flag, sample stride or 0) of a [M, D] or [B, T, D] activation."""
     f32, sh = _F32.get(t.dtype), t.shape
     if f32 is None or not t.is_cuda or len(sh) not in (2, 3):
         raise ValueError(f"{name}: expected a CUDA bf16 or fp32 tensor [rows, D] or [samples, rows, D], got {t.dtype} "
@@ -739,14 +739,15 @@ def _norm_rows(t, name, shape=None, device=None):
         raise ValueError(f"{name}: shape {tuple(sh)} on {t.device}, expected {tuple(shape)} on {device}")
     D = sh[-1]
     if t.is_contiguous():
-        return t.data_ptr(), D, f32
+        return t.data_ptr(), D, f32, 0
     st, T = t.stride(), sh[-2]
-    ld = st[-2] if T > 1 else (st[0] if len(sh) == 3 and sh[0] > 1 else D)
-    if (D > 1 and st[-1] != 1) or (len(sh) == 3 and sh[0] > 1 and T > 1 and st[0] != T * ld):
-        raise ValueError(f"{name}: rows must be contiguous and evenly spaced, got strides {st}")
-    if ld < D and sh[:-1].numel() > 1:
+    if D > 1 and st[-1] != 1:
+        raise ValueError(f"{name}: rows must be contiguous, got strides {st}")
+    ld = st[-2] if T > 1 else D
+    ss = st[0] if len(sh) == 3 and sh[0] > 1 else 0
+    if ld < D or (ss and ss < (T - 1) * ld + D):
         raise ValueError(f"{name}: rows overlap (strides {st})")
-    return t.data_ptr(), max(ld, D), f32
+    return t.data_ptr(), ld, f32, 0 if ss == T * ld else ss
 
 
 def _mod(m, name, D, samples, device, f32):
@@ -764,12 +765,12 @@ def _mod(m, name, D, samples, device, f32):
 
 _NO_NORM = (0, 0.0, 0, 0, 0, 0)
 # svdq_block_norm_args field by field, as SvdqBlockNormArgs: packing takes a fifth of filling that structure
-_PACK_NORM_ARGS = struct.Struct("@4iPPqiiPqPqPqiiPqPqPqff" + 2 * "ifiiPP").pack
+_PACK_NORM_ARGS = struct.Struct("@4iPPqiiPqPqPqiiPqPqPqff" + 2 * "ifiiPP" + "4q").pack
 
 
 def _norm_args(x, y, gate, post, res_scale, skip_scale, norm, scale, shift, offsets, out, h):
     device, shape = x.device, x.shape
-    px, ldx, x_f32 = _norm_rows(x, "x")
+    px, ldx, x_f32, sx = _norm_rows(x, "x")
     D = shape[-1]
     if offsets is not None:
         if len(shape) != 2:
@@ -789,18 +790,18 @@ def _norm_args(x, y, gate, post, res_scale, skip_scale, norm, scale, shift, offs
     for name, n in (("post", post), ("norm", norm)):
         if n is not None and n.D is not None and (n.D != D or n.device != device):
             raise ValueError(f"{name}: vectors of {n.D} on {n.device}, expected {D} on {device}")
-    py, ldy, y_f32, po, ldo = 0, 0, 0, 0, 0
+    py, ldy, y_f32, sy, po, ldo, so = 0, 0, 0, 0, 0, 0, 0
     if y is not None:
-        py, ldy, y_f32 = _norm_rows(y, "y", shape, device)
-        po, ldo, o_f32 = _norm_rows(out, "out", shape, device)
+        py, ldy, y_f32, sy = _norm_rows(y, "y", shape, device)
+        po, ldo, o_f32, so = _norm_rows(out, "out", shape, device)
         if o_f32 != x_f32:
             raise ValueError(f"out: {out.dtype}, expected x's {x.dtype}")
-    ph, ldh, h_f32 = (0, 0, 0) if h is None else _norm_rows(h, "h", shape, device)
+    ph, ldh, h_f32, sh = (0, 0, 0, 0) if h is None else _norm_rows(h, "h", shape, device)
     if M == 0:
         return None  # no row: empty tensors have no address to pass
     return _PACK_NORM_ARGS(M, D, samples, T, p_off, px, ldx, x_f32, y_f32, py, ldy, po, ldo, ph, ldh, h_f32, mod_f32,
                            p_gate, ld_gate, p_scale, ld_scale, p_shift, ld_shift, skip_scale, res_scale,
-                           *(_NO_NORM if post is None else post.fields), *(_NO_NORM if norm is None else norm.fields))
+                           *(_NO_NORM if post is None else post.fields), *(_NO_NORM if norm is None else norm.fields), sx, sy, so, sh)
 
 
 def _run_norm(a, device, w=None, act=None):

@@ -2106,12 +2106,34 @@ bool bad_norm(const svdq_norm& n) {
 }
 bool misaligned(const void* p, int f32) { return (reinterpret_cast<uintptr_t>(p) & (f32 ? 3u : 1u)) != 0; }
 
-// Byte range of M rows of D elements with row stride ld.
+// The bytes of an activation: `samples` blocks, ss apart, of `rows` rows of `row` bytes, ls apart.
 struct Span {
   uintptr_t lo, hi;
-  Span(const void* p, long long M, long long D, long long ld, int esize)
-      : lo(reinterpret_cast<uintptr_t>(p)), hi(lo + static_cast<uintptr_t>(((M - 1) * ld + D) * esize)) {}
-  bool overlaps(const Span& o) const { return lo < o.hi && o.lo < hi; }
+  uintptr_t row, ls, block, ss;
+  Span(const void* p, const svdq_block_norm_args* a, long long ld, long long sample, int f32) {
+    const uintptr_t e = f32 ? 4 : 2;
+    const bool even = a->offsets != nullptr || sample == 0 || a->M <= a->rows_per_sample;
+    const long long rows = even ? a->M : a->rows_per_sample, samples = even ? 1 : (a->M + rows - 1) / rows;
+    row = a->D * e;
+    ls = ld * e;
+    block = (rows - 1) * ls + row;
+    ss = even ? block : sample * e;
+    lo = reinterpret_cast<uintptr_t>(p);
+    hi = lo + (samples - 1) * ss + block;
+  }
+  // Whether two may share a byte: not if their ranges are apart, or if one lies in columns (or in a slice
+  // of a sample) that the other leaves out throughout.
+  bool overlaps(const Span& o) const {
+    if (hi <= o.lo || o.hi <= lo) return false;
+    const auto beside = [](uintptr_t p, uintptr_t n, uintptr_t q, uintptr_t m, uintptr_t period) {
+      const uintptr_t d = q >= p ? (q - p) % period : (period - (p - q) % period) % period;
+      return d >= n && d + m <= period;
+    };
+    if (ls == o.ls && (ss == block || ss % ls == 0) && (o.ss == o.block || o.ss % ls == 0) &&
+        beside(lo, row, o.lo, o.row, ls))
+      return false;
+    return !(ss == o.ss && ss > block && beside(lo, block, o.lo, o.block, ss));
+  }
 };
 
 svdq_status check_norm_args(const svdq_block_norm_args* a, bool quant) {
@@ -2134,9 +2156,15 @@ svdq_status check_norm_args(const svdq_block_norm_args* a, bool quant) {
   if (a->y == nullptr && (a->x_out != nullptr || a->gate != nullptr || a->post.kind != SVDQ_NORM_NONE))
     return fail(SVDQ_ERR_INVALID_ARG, "x_out, gate or a post norm without y");
   if (!wants_h && a->x_out == nullptr) return fail(SVDQ_ERR_INVALID_ARG, "no output");
-  const long long lds[] = {a->ldx, a->y ? a->ldy : a->D, a->x_out ? a->ld_out : a->D, a->h ? a->ldh : a->D};
-  for (long long ld : lds)
-    if (ld < a->D || ld >= (1ll << 38)) return fail(SVDQ_ERR_INVALID_ARG, "row stride %lld for rows of %d", ld, a->D);
+  const struct { const void* p; long long ld, ss; } acts[] = {
+      {a->x, a->ldx, a->sx}, {a->y, a->ldy, a->sy}, {a->x_out, a->ld_out, a->s_out}, {a->h, a->ldh, a->sh}};
+  for (const auto& t : acts) {
+    if (t.p == nullptr) continue;
+    if (t.ld < a->D || t.ld >= (1ll << 38))
+      return fail(SVDQ_ERR_INVALID_ARG, "row stride %lld for rows of %d", t.ld, a->D);
+    if (t.ss != 0 && (a->offsets != nullptr || t.ss < (a->rows_per_sample - 1) * t.ld + a->D || t.ss >= (1ll << 38)))
+      return fail(SVDQ_ERR_INVALID_ARG, "sample stride %lld", t.ss);
+  }
   const long long mods[] = {a->gate ? a->ld_gate : 0, a->scale ? a->ld_scale : 0, a->shift ? a->ld_shift : 0};
   for (long long ld : mods)
     if (ld < 0 || ld >= (1ll << 38)) return fail(SVDQ_ERR_INVALID_ARG, "sample stride %lld", ld);
@@ -2148,18 +2176,17 @@ svdq_status check_norm_args(const svdq_block_norm_args* a, bool quant) {
     return fail(SVDQ_ERR_UNSUPPORTED, "a pointer is not aligned to its element");
   if (a->M > 0) {
     // rows are read once, by the threads that write x_out's: x_out may be x, nothing else may overlap
-    const Span x(a->x, a->M, a->D, a->ldx, a->x_f32 ? 4 : 2);
+    const Span x(a->x, a, a->ldx, a->sx, a->x_f32);
     if (a->x_out != nullptr) {
-      const Span o(a->x_out, a->M, a->D, a->ld_out, a->x_f32 ? 4 : 2);
-      if (o.overlaps(x) && !(a->x_out == a->x && a->ld_out == a->ldx))
+      const Span o(a->x_out, a, a->ld_out, a->s_out, a->x_f32);
+      if (o.overlaps(x) && !(a->x_out == a->x && a->ld_out == a->ldx && o.ss == x.ss))
         return fail(SVDQ_ERR_INVALID_ARG, "x_out overlaps x without being x");
-      if (o.overlaps(Span(a->y, a->M, a->D, a->ldy, a->y_f32 ? 4 : 2)))
-        return fail(SVDQ_ERR_INVALID_ARG, "x_out overlaps y");
+      if (o.overlaps(Span(a->y, a, a->ldy, a->sy, a->y_f32))) return fail(SVDQ_ERR_INVALID_ARG, "x_out overlaps y");
     }
     if (a->h != nullptr) {
-      const Span h(a->h, a->M, a->D, a->ldh, a->h_f32 ? 4 : 2);
-      if (h.overlaps(x) || (a->y != nullptr && h.overlaps(Span(a->y, a->M, a->D, a->ldy, a->y_f32 ? 4 : 2))) ||
-          (a->x_out != nullptr && h.overlaps(Span(a->x_out, a->M, a->D, a->ld_out, a->x_f32 ? 4 : 2))))
+      const Span h(a->h, a, a->ldh, a->sh, a->h_f32);
+      if (h.overlaps(x) || (a->y != nullptr && h.overlaps(Span(a->y, a, a->ldy, a->sy, a->y_f32))) ||
+          (a->x_out != nullptr && h.overlaps(Span(a->x_out, a, a->ld_out, a->s_out, a->x_f32))))
         return fail(SVDQ_ERR_INVALID_ARG, "h overlaps x, y or x_out");
     }
   }
@@ -2170,7 +2197,8 @@ svdq_status check_norm_args(const svdq_block_norm_args* a, bool quant) {
 bool norm_vectorised(const svdq_block_norm_args* a) {
   if (a->D % 8 != 0) return false;
   const struct { const void* p; long long ld; int f32; } rows[] = {
-      {a->x, a->ldx, a->x_f32},         {a->y, a->ldy, a->y_f32},          {a->x_out, a->ld_out, a->x_f32},
+      {a->x, a->sx, a->x_f32},          {a->y, a->sy, a->y_f32},           {a->x_out, a->s_out, a->x_f32},
+      {a->h, a->sh, a->h_f32},          {a->x, a->ldx, a->x_f32},         {a->y, a->ldy, a->y_f32},          {a->x_out, a->ld_out, a->x_f32},
       {a->h, a->ldh, a->h_f32},         {a->gate, a->ld_gate, a->mod_f32}, {a->scale, a->ld_scale, a->mod_f32},
       {a->shift, a->ld_shift, a->mod_f32}, {a->post.weight, 0, 0},         {a->post.bias, 0, 0},
       {a->norm.weight, 0, 0},           {a->norm.bias, 0, 0}};
@@ -2262,6 +2290,11 @@ svdq_status run_norm(const svdq_block_norm_args* a, const svdq_mx_weight* w, con
   k.ldy = a->ldy;
   k.ld_out = a->ld_out;
   k.ldh = a->ldh;
+  const auto adj = [&](long long ss, long long ld) { return ss == 0 ? 0 : ss - a->rows_per_sample * ld; };
+  k.adj_x = adj(a->sx, a->ldx);
+  k.adj_y = adj(a->sy, a->ldy);
+  k.adj_out = adj(a->s_out, a->ld_out);
+  k.adj_h = adj(a->sh, a->ldh);
   k.x_f32 = a->x_f32;
   k.y_f32 = a->y_f32;
   k.h_f32 = a->h_f32;

@@ -33,7 +33,8 @@ struct Args {
   const void* y;
   void* x_out;
   void* h;
-  long long ldx, ldy, ld_out, ldh;
+  long long ldx, ldy, ld_out, ldh;   // row m of sample s: element m ld + s adj
+  long long adj_x, adj_y, adj_out, adj_h;
   int x_f32, y_f32, h_f32;
   int M, D, rows;     // rows: M, or the padded rows of a quantized output
   int samples, rows_per_sample;
@@ -330,7 +331,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) block_norm_any_kernel(const __
     if (s < 0) continue;
     float v[C][8];
     if (a.y != nullptr) {
-      load(v, a.y, m * a.ldy, a.y_f32);
+      load(v, a.y, m * a.ldy + s * a.adj_y, a.y_f32);
       if (a.post.kind) normalise(v, a.post);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
@@ -340,13 +341,13 @@ __global__ void __launch_bounds__(32 * kMaxWarps) block_norm_any_kernel(const __
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int i = index<false>(c, e, G, t);
-          const float x = i < D ? load1(a.x, m * a.ldx + i, a.x_f32) : 0.0f;
+          const float x = i < D ? load1(a.x, m * a.ldx + s * a.adj_x + i, a.x_f32) : 0.0f;
           v[c][e] = fmaf(v[c][e], f[e], fmaf(a.skip, x, b[e]));
         }
-        if (a.x_out != nullptr) store_strided(v[c], a.x_out, m * a.ld_out, a.x_f32, c, D, G, t);
+        if (a.x_out != nullptr) store_strided(v[c], a.x_out, m * a.ld_out + s * a.adj_out, a.x_f32, c, D, G, t);
       }
     } else {
-      load(v, a.x, m * a.ldx, a.x_f32);
+      load(v, a.x, m * a.ldx + s * a.adj_x, a.x_f32);
     }
     if (!a.pre.kind) continue;
     normalise(v, a.pre);
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) block_norm_any_kernel(const __
       pre_factors<false>(a, s, c, G, t, f, b);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[c][e] = fmaf(v[c][e], f[e], b[e]);
-      store_strided(v[c], a.h, m * a.ldh, a.h_f32, c, D, G, t);
+      store_strided(v[c], a.h, m * a.ldh + s * a.adj_h, a.h_f32, c, D, G, t);
     }
   }
 }
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
 
   // the first warp's place in the group's batches, `stages` ahead of the group's
   uint32_t pending = 0;  // stages whose copies are under way and not yet seen to land
-  int f_m = beg + group * R, f_end = beg;
+  int f_m = beg + group * R, f_end = beg, f_s = 0;
   auto fetch = [&](int stage) {
     if (t >= 32) return;
     while (f_m >= f_end) {  // into the next run that holds a batch of this group
@@ -446,6 +447,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
       const Run r = run_at(a, f_end, end);
       f_m = r.s >= 0 ? f_end + group * R : r.end;
       f_end = r.end;
+      f_s = r.s;
     }
     if (*abort_flag) return;
     const uint32_t n = min(R, f_end - f_m);
@@ -455,8 +457,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
     if (lane < n) {
       const uint32_t dst = smem_addr(ring + stage * stage_bytes + lane * row_bytes);
       const long long m = f_m + lane;
-      bulk_load(dst, static_cast<const uint8_t*>(a.x) + m * a.ldx * xs, D * xs, bar);
-      if (has_y) bulk_load(dst + x_span, static_cast<const uint8_t*>(a.y) + m * a.ldy * ys, D * ys, bar);
+      bulk_load(dst, static_cast<const uint8_t*>(a.x) + (m * a.ldx + f_s * a.adj_x) * xs, D * xs, bar);
+      if (has_y) bulk_load(dst + x_span, static_cast<const uint8_t*>(a.y) + (m * a.ldy + f_s * a.adj_y) * ys, D * ys, bar);
     }
     pending |= 1u << stage;
     f_m += step;
@@ -627,7 +629,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
 #pragma unroll
           for (int r = 0; r < R; ++r) rstd[r] = root(rstd[r], inv_d, a.post.eps);
         }
-        uint8_t* const x_row = static_cast<uint8_t*>(a.x_out) + m * out_step;
+        uint8_t* const x_row = static_cast<uint8_t*>(a.x_out) + m * out_step + s * a.adj_out * xs;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           F8 f;
@@ -707,7 +709,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
       red.sum(rstd);
 #pragma unroll
       for (int r = 0; r < R; ++r) rstd[r] = root(rstd[r], inv_d, a.pre.eps);
-      uint8_t* const h_row = static_cast<uint8_t*>(a.h) + m * h_step;
+      uint8_t* const h_row = static_cast<uint8_t*>(a.h) + m * h_step + s * a.adj_h * (h_f32 ? 4 : 2);
       const long long code_step = a.K_pad >> 1;
       uint8_t* const code_row = a.codes + m * code_step;
 #pragma unroll

@@ -33,8 +33,9 @@
  *     asynchronous; argument checks happen on the host before anything is enqueued, and on a
  *     failed check nothing is enqueued.
  *   - The per-call kernels are launched with programmatic stream serialization: one may start its
- *     set-up (barriers, tensor memory) while the kernel before it on the stream is finishing, but
- *     it reads or writes no global memory until that kernel has completed. Stream order is kept.
+ *     set-up (barriers, tensor memory; svdq_mx_gemm for few rows also prefetches weight lines into
+ *     L2) while the kernel before it on the stream is finishing, but it reads or writes no global
+ *     memory until that kernel has completed. Stream order is kept.
  *   - Shapes: K % 256 == 0; N % n_tile == 0 for the n_tile chosen at pack time (384 for a weight
  *     without SwiGLU where 768 divides N, else 256 where it divides N, else 192, else 128; SwiGLU
  *     needs N even); r in {0, 16, 32, 64}; 1 <= M < 2^24.
@@ -387,11 +388,14 @@ SVDQ_API svdq_status svdq_mx_dequantize_act(const svdq_mx_act* act, void* out, l
  *           = v / sqrt(mean(v^2) + eps) . weight (+ bias)     (SVDQ_NORM_RMS)
  * s is the row's sample; . is elementwise; absent vectors act as 1 (weight, gate) or 0 (bias, scale,
  * shift). Everything is computed in fp32; x' and h are rounded once, when stored (h from the unrounded
- * x'). Rows: M rows of D values with row strides (elements). Samples: without offsets row m belongs to
- * sample m / rows_per_sample; with offsets (device int32 [samples + 1], ascending) sample s has rows
- * offsets[s] .. offsets[s + 1] - 1, and rows outside every sample are neither read nor written.
- * x_out may be x itself (same stride); h must not overlap an input. 1 <= D <= 32768; any strides and
- * element alignment (16-byte aligned rows and vectors with D a multiple of 8 take the fast path). */
+ * x'). Rows: M rows of D values. Without offsets row m is row t = m % rows_per_sample of sample s = m /
+ * rows_per_sample, at s * sample stride + t * row stride (elements; a sample stride of 0 stands for
+ * rows_per_sample * row stride), so that a tensor may be a slice of tokens or columns of a larger one.
+ * With offsets (device int32 [samples + 1], ascending) sample s has rows offsets[s] .. offsets[s + 1] - 1
+ * at m * row stride, and rows outside every sample are neither read nor written.
+ * x_out may be x itself (same strides); no other output may share memory with an input or output.
+ * 1 <= D <= 32768; any strides and element alignment (16-byte aligned rows and vectors with D a
+ * multiple of 8 take the fast path). */
 typedef enum { SVDQ_NORM_NONE = 0, SVDQ_NORM_RMS = 1, SVDQ_NORM_LAYER = 2 } svdq_norm_kind;
 
 typedef struct svdq_norm {   /* one normalisation: kind, eps and its vectors */
@@ -418,6 +422,7 @@ typedef struct svdq_block_norm_args {
   float skip_scale, res_scale;
   svdq_norm post;                       /* of y; kind NONE: identity                     */
   svdq_norm norm;                       /* of x'; kind NONE with h == NULL only          */
+  long long sx, sy, s_out, sh;          /* sample strides; 0 with offsets or even rows   */
 } svdq_block_norm_args;
 
 SVDQ_API svdq_status svdq_block_norm(const svdq_block_norm_args* a, svdq_stream_t stream);

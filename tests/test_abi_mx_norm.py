@@ -166,6 +166,8 @@ NORM_BAD = [
     (dict(ldx=39), 1), (dict(ldy=0), 1), (dict(ldh=-40), 1), (dict(ld_gate=-1), 1),
     (dict(x=BASE + 1), 2), (dict(gate=BASE + (4 << 20) + 2, mod_f32=1), 2), (dict(norm__weight=BASE + (5 << 20) + 1), 2),
     (dict(x_out=BASE + 80), 1),                                         # shifted over x
+    (dict(sx=239), 1), (dict(sh=-1), 1), (dict(s_out=1 << 38), 1),        # sample strides
+    (dict(sx=400, x_out=BASE), 1),                                      # in place with other strides
     (dict(x_out=BASE, ld_out=48), 1), (dict(x_out=BASE + (1 << 20)), 1),
     (dict(h=BASE), 1), (dict(h=BASE + (1 << 20) + 64), 1), (dict(h=BASE + (2 << 20)), 1),
 ]
@@ -177,7 +179,8 @@ def test_block_norm_refusals(L, change, status):
 
 
 @pytest.mark.parametrize("change", [{}, dict(x_out=BASE), dict(h=None, norm__kind=0), dict(x_out=None),
-                                    dict(y=None, x_out=None, gate=None), dict(ldx=41, x=BASE + 2)])
+                                    dict(y=None, x_out=None, gate=None), dict(ldx=41, x=BASE + 2),
+                                    dict(ldx=80, ldh=80, h=BASE + 80), dict(sx=480, sh=480, h=BASE + 480)])
 def test_block_norm_well_formed(L, change):
     if torch.cuda.is_available():
         pytest.skip("fake addresses: CPU only")

@@ -130,18 +130,19 @@ def test_code_edges(cuda_device):
     assert np.array_equal(svdq.dequantize_act_mx(act, out_dtype=torch.float32).cpu().double().numpy(), want)
 
 
-def test_non_finite_blocks_poison_their_rows_only(cuda_device):
-    X, prep, _ = _layer(40, 320, 256, 0, 11)
+@pytest.mark.parametrize("M", [40, 400, 1100])
+def test_non_finite_blocks_poison_their_rows_only(cuda_device, M):
+    X, prep, _ = _layer(M, 320, 256, 0, 11)
     Xd = to_dev_bf16(X, cuda_device)
     Xd[3, 100], Xd[17, 319], Xd[20, 0] = float("nan"), float("inf"), float("-inf")
     w = _weight(prep, cuda_device)
-    act = svdq.quantize_act_mx(Xd, w, svdq.MxAct(40, 320, 0, cuda_device))
+    act = svdq.quantize_act_mx(Xd, w, svdq.MxAct(M, 320, 0, cuda_device))
     _, s = svdq.export_act_mx(act)
     bad = {(3, 3), (17, 9), (20, 0)}
     assert {tuple(i) for i in torch.nonzero(s == 255).tolist()} == bad
     assert torch.isnan(svdq.dequantize_act_mx(act)[17, 288:]).all()
     y = svdq.gemm_mx(act, w)
-    clean = torch.ones(40, dtype=torch.bool)
+    clean = torch.ones(M, dtype=torch.bool)
     clean[[3, 17, 20]] = False
     assert torch.isnan(y[~clean.to(y.device)]).all() and torch.isfinite(y[clean.to(y.device)]).all()
 
