@@ -1445,7 +1445,7 @@ constexpr int kMxStages384 = 4;
 constexpr int kMxStages256 = 5;
 constexpr int kMxStages128 = 7;
 template <int N_TILE, int STAGES>
-using MxLayout = svdq::PairGemmLayout<true, N_TILE, STAGES, svdq::mx::Gemm::kSfAtomsK>;
+using MxLayout = svdq::PairGemmLayout<true, N_TILE, STAGES, svdq::mx::Gemm::kSfAtomsK, svdq::mx::Gemm::kBiasSmem>;
 
 struct MxState {
   bool ready = false;

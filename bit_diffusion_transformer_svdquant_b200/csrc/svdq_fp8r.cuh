@@ -230,6 +230,7 @@ struct Fp8Gemm {
   using Args = GemmArgs;
   static constexpr bool kScales = false;
   static constexpr int kSfAtomsK = 4;  // of no effect without scale factors
+  static constexpr bool kBiasSmem = false;
   template <int N_TILE>
   __device__ static int b_row(const Args&, int n_blk, int rank) {
     return n_blk * N_TILE + rank * (N_TILE / 2);

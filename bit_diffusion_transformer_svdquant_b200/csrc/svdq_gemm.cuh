@@ -68,8 +68,8 @@ struct GemmArgs {
 // Shared memory and TMEM layout of the pair GEMM. SCALES: a block-scaled format, whose ring slots
 // also carry the K step's scale atoms and whose scale factors sit in TMEM buffers. SF_K: atoms of
 // 128 rows x 4 scales that a 256-wide K step takes per 128 rows (4 at one scale per 16 elements, 2 at
-// one per 32).
-template <bool SCALES, int N_TILE, int STAGES, int SF_K = 4>
+// one per 32). BIAS: the epilogue warps keep their columns' biases in shared memory as fp32.
+template <bool SCALES, int N_TILE, int STAGES, int SF_K = 4, bool BIAS = false>
 struct PairGemmLayout {
   static constexpr int kBRows = N_TILE / 2;  // rows of B staged by each CTA of the pair
   static constexpr int kA = 128 * 128;       // 128 rows x 128 bytes of codes (one K step)
@@ -93,7 +93,9 @@ struct PairGemmLayout {
   // epilogue staging: 8 warps x 4 KB (two 32 x 32 bf16 boxes or one fp32 box in flight)
   static constexpr int kStageOutWarp = 4096;
   static constexpr int kOutOff = STAGES * kStage;
-  static constexpr int kBarOff = kOutOff + 8 * kStageOutWarp;
+  static constexpr int kBiasOff = kOutOff + 8 * kStageOutWarp;
+  static constexpr int kBiasWarp = BIAS ? (N_TILE / 2) * 4 : 0;
+  static constexpr int kBarOff = kBiasOff + 8 * kBiasWarp;
   // full[STAGES], empty[STAGES], sf_land[STAGES], accf[kAccBufs], acce[kAccBufs], drain, sf_full[kSfBufs]
   static constexpr int kNumBars = 3 * STAGES + 2 * kAccBufs + 1 + kSfBufs;
   static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + 1024;
@@ -149,6 +151,7 @@ struct Nvfp4Gemm {
   static constexpr bool kScales = true;
   static constexpr int kSfAtomsK = 4;
   static constexpr bool kL2HiLo = false;
+  static constexpr bool kBiasSmem = false;
   // first row of B that CTA `rank` of the pair stages for tile n_blk
   template <int N_TILE>
   __device__ static int b_row(const Args&, int n_blk, int rank) {
@@ -235,7 +238,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                      const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmL2,
                      const __grid_constant__ CUtensorMap tmY, const typename F::Args args) {
   constexpr int kSfK = F::kSfAtomsK;
-  using L = PairGemmLayout<F::kScales, N_TILE, STAGES, kSfK>;
+  using L = PairGemmLayout<F::kScales, N_TILE, STAGES, kSfK, F::kBiasSmem>;
   constexpr int kSfBufs = L::kSfBufs, kAccBufs = L::kAccBufs;
   extern __shared__ uint8_t smem_raw[];
   // the same offsets in both CTAs: the pair MMA addresses the odd CTA's operands by this CTA's
@@ -590,20 +593,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
       store_box(dst, row0, col0);
     };
+    // biases of output columns n0..: with kBiasSmem this warp's fp32 copies, whose column `l` (of the
+    // warp's plain columns; with SwiGLU of its gate columns, then its up columns) is n0
+    float* const bias_s = reinterpret_cast<float*>(smem + L::kBiasOff + (warp - 2) * L::kBiasWarp);
+    auto bias_of = [&](int n0, int l) {
+      if constexpr (F::kBiasSmem) {
+        (void)n0;
+        return static_cast<const float*>(bias_s + l);
+      } else {
+        (void)l;
+        return args.bias + n0;
+      }
+    };
     // y = scale(g) * acc (+ bias[n]) for 8 values of accumulator (GEMM) columns g0.. and output
     // (bias) columns n0..
     // (v is a register array; `off` is a compile-time constant after unrolling, so it stays one)
-    auto affine8 = [&](const typename F::Epi& ep, auto& v, int off, int g0, int n0) {
-      if (has_bias) ep.template apply8<true>(args, v, off, g0, args.bias + n0);
-      else ep.template apply8<false>(args, v, off, g0, nullptr);
+    auto affine8 = [&](const typename F::Epi& ep, auto& v, int off, int g0, int n0, int l) {
+      if (has_bias) ep.template apply8<true>(args, v, off, g0, bias_of(n0, l));
+      else ep.template apply8<false>(args, v, off, g0, bias_of(0, 0));
     };
-    auto affine = [&](const typename F::Epi& ep, float (&v)[32], int g0, int n0) {
+    auto affine = [&](const typename F::Epi& ep, float (&v)[32], int g0, int n0, int l) {
       if (has_bias) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) ep.template apply8<true>(args, v, i, g0 + i, args.bias + n0 + i);
+        for (int i = 0; i < 32; i += 8) ep.template apply8<true>(args, v, i, g0 + i, bias_of(n0 + i, l + i));
       } else {
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) ep.template apply8<false>(args, v, i, g0 + i, nullptr);
+        for (int i = 0; i < 32; i += 8) ep.template apply8<false>(args, v, i, g0 + i, bias_of(0, 0));
       }
     };
     auto release_acc = [&]() {
@@ -616,6 +631,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       int m_pair, n_blk;
       tile_coords(tile, args.m_pairs, args.n_tiles, m_pair, n_blk);
       const int m_blk = 2 * m_pair + static_cast<int>(rank);
+      if constexpr (F::kBiasSmem) {
+        // while the tile's MMAs run: loads and conversions here would sit between the accumulator's
+        // completion and its release
+        if (has_bias) {
+          __syncwarp();
+          const int n_cols = swiglu ? hN : args.N;
+#pragma unroll
+          for (int i = 0; i < kPlainPerWarp; ++i) {
+            const int half = kPlainPerWarp / 2;
+            const int l = (swiglu ? i % half : i) * 32 + lane;  // of this warp's output columns
+            const int n = swiglu ? n_blk * (N_TILE / 2) + glu_beg * 32 + l : n_blk * N_TILE + h * kPlainPerWarp * 32 + l;
+            const int at = n + (swiglu && i >= half ? hN : 0);
+            bias_s[i * 32 + lane] = n < n_cols ? __bfloat162float(args.bias[at]) : 0.0f;
+          }
+          __syncwarp();
+        }
+      }
       // warp-uniform outcome: tcgen05.ld below is a .sync.aligned warp instruction
       const bool got = mbar_wait_bounded(accf_bar(acc), acc_phase, wait_ns, status, kStatusEpilogue, abort_flag);
       if (!__all_sync(0xffffffffu, got)) break;
@@ -631,14 +663,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         // after the last round's loads and only then are the boxes stored (measured on B200:
         // staging and storing each chunk before the next load took ~700 cycles per chunk, all of it
         // on the issuer's path to the next tile). The 384-wide tile's six chunks per warp load their
-        // last two rounds one chunk at a time, which keeps the packed chunks and the loaded ones
-        // within the register budget.
+        // last two rounds one chunk at a time (all of them with biases in shared memory, whose reads
+        // take registers: loading pairs spilled 360 bytes and made the 16896x3072x9216 MXFP4 GEMM 227
+        // instead of 200 us), which keeps the packed chunks and the loaded ones within the register budget.
+        constexpr int kSingle = F::kBiasSmem ? 0 : 4;
         const int c_beg = h * kPlainPerWarp;
         uint32_t pk[kPlainPerWarp > 2 ? kPlainPerWarp - 2 : 1][16];
         boxes_free();
 #pragma unroll
-        for (int i = 0; i < kPlainPerWarp; i += (kPlainPerWarp > 4 && i >= 4) ? 1 : 2) {
-          const bool pair = !(kPlainPerWarp > 4 && i >= 4) && i + 1 < kPlainPerWarp;
+        for (int i = 0; i < kPlainPerWarp; i += (kPlainPerWarp > 4 && i >= kSingle) ? 1 : 2) {
+          const bool pair = !(kPlainPerWarp > 4 && i >= kSingle) && i + 1 < kPlainPerWarp;
           float v[2][32];
           tmem_ld_32x32(tb + (c_beg + i) * 32, v[0]);
           if (pair) tmem_ld_32x32(tb + (c_beg + i + 1) * 32, v[1]);
@@ -649,7 +683,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             const int j = i + u;
             if (j < kPlainPerWarp && (u == 0 || pair)) {
               const int g0 = n_blk * N_TILE + (c_beg + j) * 32;
-              affine(ep, v[u], g0, g0);
+              affine(ep, v[u], g0, g0, j * 32);
               if (j < 2) {
                 uint32_t t[16];
                 pack_bf16(v[u], t);
@@ -680,7 +714,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           tmem_wait_ld();
           if (i + 1 == kPlainPerWarp) release_acc();
           const int g0 = n_blk * N_TILE + (c_beg + i) * 32;
-          affine(ep, v, g0, g0);
+          affine(ep, v, g0, g0, i * 32);
           emit_f32(v, row0, g0);
         }
       } else if constexpr (N_TILE <= 256) {
@@ -719,8 +753,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
               uint8_t* box_row = stage_out + (hc >> 1) * 2048 + lane * 64;
 #pragma unroll
               for (int i = 0; i < 16; i += 8) {
-                affine8(ep, gg, i, g0 + i, j0 + i);
-                affine8(ep, uu, i, g0 + kHalf + i, hN + j0 + i);
+                const int l = off - glu_beg * 32 + i;
+                affine8(ep, gg, i, g0 + i, j0 + i, l);
+                affine8(ep, uu, i, g0 + kHalf + i, hN + j0 + i, kPlainPerWarp * 16 + l);
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
@@ -750,8 +785,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             if (c + 1 == n_mine) release_acc();
             const int j0 = n_blk * kHalf + cc * 32;
             const int g0 = n_blk * N_TILE + cc * 32;
-            affine(ep, gt, g0, j0);
-            affine(ep, up, g0 + kHalf, hN + j0);
+            affine(ep, gt, g0, j0, c * 32);
+            affine(ep, up, g0 + kHalf, hN + j0, kPlainPerWarp * 16 + c * 32);
             // the same arithmetic as the bf16 path, so that bf16 output = bf16(fp32 output)
 #pragma unroll
             for (int i = 0; i < 32; ++i) gt[i] = silu_times(gt[i], up[i]);

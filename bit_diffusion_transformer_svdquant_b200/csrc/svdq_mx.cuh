@@ -88,6 +88,15 @@ __device__ __forceinline__ uint32_t quarter_block(const float2 (&v)[4], uint32_t
   return s == 255u ? 0u : codes;
 }
 
+// Two IEEE round-to-nearest fp32 sums in one instruction.
+__device__ __forceinline__ float2 add2_rn(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&r);
+}
+
 // ---------------------------------------------------------------- kernel 1
 struct ActArgs {
   const float* inv_lambda;  // [K] (padded K)
@@ -197,6 +206,7 @@ struct Gemm {
   static constexpr bool kScales = true;
   static constexpr int kSfAtomsK = 2;
   static constexpr bool kL2HiLo = false;
+  static constexpr bool kBiasSmem = true;
   // The 128-wide kernel also takes a weight packed 256 or 384 wide: a block of 128 tile columns is two runs
   // of 64 packed rows, one for each CTA of the pair, and one scale atom per 128 of K.
   template <int N_TILE>
@@ -242,18 +252,21 @@ struct Gemm {
       }
     }
   }
-  // y = acc (+ bias); columns past N (padding of the last tile, clipped by the store) take the last bias
-  // columns instead of reading past the end
+  // y = acc (+ bias)
   struct Epi {
     __device__ Epi(const Args&, int) {}
     template <bool BIAS, class V>
-    __device__ void apply8(const Args& a, V& v, int off, int, const __nv_bfloat16* bias8) const {
+    __device__ void apply8(const Args&, V& v, int off, int, const float* bias8) const {
       if constexpr (BIAS) {
-        const __nv_bfloat16* last = a.bias + (a.N - 8);
-        float b[8];
-        bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(bias8 < last ? bias8 : last)), b);
+        const float4 b0 = reinterpret_cast<const float4*>(bias8)[0], b1 = reinterpret_cast<const float4*>(bias8)[1];
+        const float2 b[4] = {make_float2(b0.x, b0.y), make_float2(b0.z, b0.w), make_float2(b1.x, b1.y),
+                             make_float2(b1.z, b1.w)};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[off + j] += b[j];
+        for (int j = 0; j < 4; ++j) {
+          const float2 y = add2_rn(make_float2(v[off + 2 * j], v[off + 2 * j + 1]), b[j]);
+          v[off + 2 * j] = y.x;
+          v[off + 2 * j + 1] = y.y;
+        }
       }
     }
   };
