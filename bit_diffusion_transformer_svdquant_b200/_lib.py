@@ -102,6 +102,7 @@ def _declare(lib):
         "svdq_mx_act_bind": (c_int, [c_int, c_int, c_int, c_void_p, c_size_t, MA]),
         "svdq_mx_quantize_act": (c_int, [c_void_p, c_longlong, MW, MA, c_void_p]),
         "svdq_mx_gemm": (c_int, [MA, MW, c_void_p, c_int, c_void_p, c_longlong, c_int, c_void_p]),
+        "svdq_mx_linear": (c_int, [c_void_p, c_longlong, MW, MA, c_void_p, c_int, c_void_p, c_longlong, c_int, c_void_p]),
         "svdq_mx_export_weight": (c_int, [MW, c_void_p, c_void_p, c_void_p]),
         "svdq_mx_export_act": (c_int, [MA, c_void_p, c_void_p, c_void_p]),
         "svdq_mx_dequantize_act": (c_int, [MA, c_void_p, c_longlong, c_int, c_void_p]),
@@ -496,17 +497,16 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _enqueue(device, *calls):
-    """Each call (entry point, arguments before the stream) on the device's current stream."""
+def _enqueue(device, call):
+    """A call (entry point, its arguments before the stream) on the device's current stream."""
     index = device.index
     if index != torch.cuda.current_device():
         with torch.cuda.device(index):
-            return _enqueue(device, *calls)
-    l, stream = _lib or lib(), _raw_stream(index)
-    for name, *args in calls:
-        status = getattr(l, name)(*args, stream)
-        if status:
-            _check(name, status)
+            return _enqueue(device, call)
+    name, *args = call
+    status = getattr(_lib or lib(), name)(*args, _raw_stream(index))
+    if status:
+        _check(name, status)
 
 
 def _rows(t, dtype, name, rows, dim, device=None):
@@ -662,9 +662,9 @@ def gemm_mx(act: MxAct, w: MxWeight, bias: torch.Tensor | None = None, epilogue:
 def linear_mx(X, w: MxWeight, bias=None, act: MxAct | None = None, out=None, out_dtype=torch.bfloat16):
     """The whole MXFP4 layer on the current stream (the format has no tensor scale to calibrate)."""
     act = MxAct(X.shape[0], w.K, w.r, X.device) if act is None else act
-    quantize = _check_quantize_mx(X, w, act)
-    out, gemm_call = _check_gemm_mx(act, w, bias, None, out_dtype, out)
-    _enqueue(act.device, quantize, gemm_call)
+    _, *x_args, _, _ = _check_quantize_mx(X, w, act)
+    out, (_, act_ref, w_ref, *gemm_args) = _check_gemm_mx(act, w, bias, None, out_dtype, out)
+    _enqueue(act.device, ("svdq_mx_linear", *x_args, w_ref, act_ref, *gemm_args))
     return out
 
 

@@ -1947,8 +1947,12 @@ svdq_status svdq_mx_quantize_act(const uint16_t* X, long long ldx, const svdq_mx
   return check_launch("quant_act_kernel (MXFP4)");
 }
 
-svdq_status svdq_mx_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const uint16_t* bias, svdq_epilogue epi,
-                         void* Y, long long ldy, svdq_out_dtype out_dtype, svdq_stream_t stream) {
+}  // extern "C"
+
+namespace {
+
+svdq_status check_mx_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const uint16_t* bias, svdq_epilogue epi,
+                          const void* Y, long long ldy, svdq_out_dtype out_dtype) {
   if (act == nullptr || w == nullptr || Y == nullptr) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
   if (act->K != w->K || act->r != w->r) return fail(SVDQ_ERR_INVALID_ARG, "act does not match weight");
   if (svdq_status s = check_mx_weight(w); s != SVDQ_OK) return s;
@@ -1964,12 +1968,21 @@ svdq_status svdq_mx_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const 
   if (!aligned16(Y) || (bias != nullptr && !aligned16(bias))) return fail(SVDQ_ERR_UNSUPPORTED, "Y / bias alignment");
   if (ldy < n_out || (ldy * esize) % 16 != 0 || ldy >= (1ll << 37))
     return fail(SVDQ_ERR_UNSUPPORTED, "row stride %lld of Y: whole 16-byte units and at least %d", ldy, n_out);
+  return SVDQ_OK;
+}
+
+// svdq_mx_gemm on checked arguments.
+svdq_status mx_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const uint16_t* bias, svdq_epilogue epi, void* Y,
+                    long long ldy, svdq_out_dtype out_dtype, svdq_stream_t stream) {
+  const bool has_bias = (epi & 1) != 0, swiglu = (epi & 2) != 0;
+  const int n_out = swiglu ? w->N / 2 : w->N, esize = out_dtype == SVDQ_OUT_F32 ? 4 : 2;
   int dev, sms;
   if (svdq_status s = mx_ready(&dev, &sms); s != SVDQ_OK) return s;
 
   if (mx_few_product_rows(act->M, act->K_pad)) {
     bool done = false;
-    if (svdq_status s = mx_few_gemm(act, w, bias, has_bias, swiglu, Y, ldy, esize, dev, stream, &done); s != SVDQ_OK || done)
+    if (svdq_status s = mx_few_gemm(act, w, bias, has_bias, swiglu, Y, ldy, esize, dev, stream, &done);
+        s != SVDQ_OK || done)
       return s;
   }
   const int r = w->r, n_tile = w->n_tile;
@@ -2040,6 +2053,24 @@ svdq_status svdq_mx_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const 
                          MxLayout<128, kMxStages128>::kSmem, st, tmA, tmB, tmU, tmL2, tmY, g);
   if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, "launch of pair_gemm_kernel failed: %s", cudaGetErrorString(e));
   return check_launch("pair_gemm_kernel (MXFP4)");
+}
+
+}  // namespace
+
+extern "C" {
+
+svdq_status svdq_mx_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const uint16_t* bias, svdq_epilogue epi,
+                         void* Y, long long ldy, svdq_out_dtype out_dtype, svdq_stream_t stream) {
+  if (svdq_status s = check_mx_gemm(act, w, bias, epi, Y, ldy, out_dtype); s != SVDQ_OK) return s;
+  return mx_gemm(act, w, bias, epi, Y, ldy, out_dtype, stream);
+}
+
+svdq_status svdq_mx_linear(const uint16_t* X, long long ldx, const svdq_mx_weight* w, const svdq_mx_act* act,
+                           const uint16_t* bias, svdq_epilogue epi, void* Y, long long ldy, svdq_out_dtype out_dtype,
+                           svdq_stream_t stream) {
+  if (svdq_status s = check_mx_gemm(act, w, bias, epi, Y, ldy, out_dtype); s != SVDQ_OK) return s;
+  if (svdq_status s = svdq_mx_quantize_act(X, ldx, w, act, stream); s != SVDQ_OK) return s;
+  return mx_gemm(act, w, bias, epi, Y, ldy, out_dtype, stream);
 }
 
 svdq_status svdq_mx_export_weight(const svdq_mx_weight* w, uint8_t* codes, uint8_t* scales, svdq_stream_t stream) {

@@ -26,9 +26,6 @@ constexpr int kFewCols = 128;  // the product's tokens at most
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void prefetch_l2_2d(const CUtensorMap* map, int x, int y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
-}
 
 // ---------------------------------------------------------------- quantizer
 struct FewQuantArgs {
@@ -223,8 +220,9 @@ __host__ __device__ constexpr int few_part_bytes(int NB, int cols) { return NB *
 // NB = 1: block b of 128 output columns (weight rows in tile order). NB = 2 (SwiGLU, n_tile 256): gate and
 // up rows of 128 outputs, in two accumulators. Cluster rank c sums K steps [c n / ranks, (c + 1) n / ranks)
 // of n; rank 0 also the low-rank branch.
-// The weight is not written by the kernel before this one in a layer call; its lines are prefetched into
-// L2 (a hint that orders nothing) while that kernel still runs, and read after it.
+// Everything is read after the kernel before has completed. Reading the weight while the quantizer runs, into
+// the ring (10.7 -> 11.8 us) or only into L2 (11.6 us), made a layer of one token slower, not faster (3072 ->
+// 9216, r = 32, weight in L2): the quantizer's own loads wait behind it.
 template <int NB>
 __global__ void __launch_bounds__(kFewThreads, 1)
     few_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -268,11 +266,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     mbar_init(drain_bar, 1);
     abort_smem = 0;
     fence_barrier_init();
-    for (int k = k_beg; k < k_end; ++k)
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) prefetch_l2_2d(&tmW, k * 128, packed_row(b, h));
   }
   if (warp == 1) {
     tmem_alloc(smem_addr(&tmem_slot), a.tmem_cols);
@@ -282,6 +275,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (ranks > 1) cluster_arrive();  // waited for before the first write into another CTA
+  const int slots = lr_slots + k_end - k_beg;
   grid_dependency_wait();
   grid_launch_dependents();
   const uint32_t tmem = tmem_slot;
@@ -291,45 +285,36 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0, armed = 0, armed_parity = 0;
-      bool ok = true;
-      auto take = [&](uint32_t bytes) {  // waits for the stage and arms it
-        ok = mbar_wait_bounded(empty_bar(stage), phase ^ 1u, a.wait_ns, status, kStatusProducer, abort_flag);
-        if (!ok) return false;
-        mbar_arrive_expect_tx(full_bar(stage), bytes);
+      for (int slot = 0; slot < slots; ++slot) {
+        if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, a.wait_ns, status, kStatusProducer, abort_flag)) break;
+        const uint32_t sa = sbase + stage * stage_bytes, fb = full_bar(stage);
         armed |= 1u << stage;
         armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-        return true;
-      };
-      auto next = [&] {
-        if (++stage == stages) { stage = 0; phase ^= 1u; }
-      };
-      for (int c = 0; ok && c < lr_slots; ++c) {
-        if (!take(static_cast<uint32_t>((NB * 128 + 2 * cols) * rc * 2))) break;
-        const uint32_t sa = sbase + stage * stage_bytes, fb = full_bar(stage);
+        if (slot < lr_slots) {
+          mbar_arrive_expect_tx(fb, static_cast<uint32_t>((NB * 128 + 2 * cols) * rc * 2));
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+          for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            tma_load_2d(sa + (b * 128 + h * 64) * rc * 2, &tmL2, c * kLrChunk, packed_row(b, h), fb);
-        tma_load_2d(sa + off_x, &tmU, c * kLrChunk, 0, fb);
-        tma_load_2d(sa + off_x + cols * rc * 2, &tmU, c * kLrChunk, a.M_pad, fb);
-        next();
-      }
-      for (int k = k_beg; ok && k < k_end; ++k) {
-        if (!take(static_cast<uint32_t>(stage_bytes))) break;
-        const uint32_t sa = sbase + stage * stage_bytes, fb = full_bar(stage);
+            for (int h = 0; h < 2; ++h)
+              tma_load_2d(sa + (b * 128 + h * 64) * rc * 2, &tmL2, slot * kLrChunk, packed_row(b, h), fb);
+          tma_load_2d(sa + off_x, &tmU, slot * kLrChunk, 0, fb);
+          tma_load_2d(sa + off_x + cols * rc * 2, &tmU, slot * kLrChunk, a.M_pad, fb);
+        } else {
+          const int k = k_beg + slot - lr_slots;
+          mbar_arrive_expect_tx(fb, static_cast<uint32_t>(stage_bytes));
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
+          for (int b = 0; b < NB; ++b) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) tma_load_2d(sa + b * 16384 + h * 8192, &tmW, k * 128, packed_row(b, h), fb);
+            for (int h = 0; h < 2; ++h) tma_load_2d(sa + b * 16384 + h * 8192, &tmW, k * 128, packed_row(b, h), fb);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            bulk_load(sa + off_sfw + (b * 2 + i) * 512,
-                      a.sfw + (((static_cast<size_t>(nb0) * (a.K >> 7) + 2 * k + i) * atoms + at + b) << 9), 512, fb);
+            for (int i = 0; i < 2; ++i)
+              bulk_load(sa + off_sfw + (b * 2 + i) * 512,
+                        a.sfw + (((static_cast<size_t>(nb0) * (a.K >> 7) + 2 * k + i) * atoms + at + b) << 9), 512, fb);
+          }
+          tma_load_2d(sa + off_x, &tmX, k * 128, 0, fb);
+          bulk_load(sa + off_sfx, a.sfx + (static_cast<size_t>(2 * k) << 9), 1024, fb);
         }
-        tma_load_2d(sa + off_x, &tmX, k * 128, 0, fb);
-        bulk_load(sa + off_sfx, a.sfx + (static_cast<size_t>(2 * k) << 9), 1024, fb);
-        next();
+        if (++stage == stages) { stage = 0; phase ^= 1u; }
       }
       // every copy this thread started has landed before the CTA may leave
       for (int s = 0; s < stages; ++s)
@@ -343,7 +328,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       bool ok = true;
       const uint32_t id_lr = idesc_bf16(128, cols);
       const uint32_t id0 = idesc_mxf4(128, cols, 0), id2 = idesc_mxf4(128, cols, 2);
-      for (int slot = 0; slot < lr_slots + k_end - k_beg; ++slot) {
+      for (int slot = 0; slot < slots; ++slot) {
         if (!(ok = mbar_wait_bounded(full_bar(stage), phase, a.wait_ns, status, kStatusMma, abort_flag))) break;
         tc_fence_after();
         const uint32_t sa = sbase + stage * stage_bytes;

@@ -33,9 +33,8 @@
  *     asynchronous; argument checks happen on the host before anything is enqueued, and on a
  *     failed check nothing is enqueued.
  *   - The per-call kernels are launched with programmatic stream serialization: one may start its
- *     set-up (barriers, tensor memory; svdq_mx_gemm for few rows also prefetches weight lines into
- *     L2) while the kernel before it on the stream is finishing, but it reads or writes no global
- *     memory until that kernel has completed. Stream order is kept.
+ *     set-up (barriers, tensor memory) while the kernel before it on the stream is finishing, but
+ *     it reads or writes no global memory until that kernel has completed. Stream order is kept.
  *   - Shapes: K % 256 == 0; N % n_tile == 0 for the n_tile chosen at pack time (384 for a weight
  *     without SwiGLU where 768 divides N, else 256 where it divides N, else 192, else 128; SwiGLU
  *     needs N even); r in {0, 16, 32, 64}; 1 <= M < 2^24.
@@ -364,6 +363,12 @@ SVDQ_API svdq_status svdq_mx_quantize_act(const uint16_t* X, long long ldx, cons
 SVDQ_API svdq_status svdq_mx_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const uint16_t* bias,
                          svdq_epilogue epi, void* Y, long long ldy, svdq_out_dtype out_dtype,
                          svdq_stream_t stream);
+
+/* The whole layer: svdq_mx_quantize_act, then svdq_mx_gemm on its result. The arguments of both are checked
+ * before anything is enqueued. */
+SVDQ_API svdq_status svdq_mx_linear(const uint16_t* X, long long ldx, const svdq_mx_weight* w, const svdq_mx_act* act,
+                           const uint16_t* bias, svdq_epilogue epi, void* Y, long long ldy,
+                           svdq_out_dtype out_dtype, svdq_stream_t stream);
 
 /* Debug / parity: canonical codes [rows][K/2] and scale codes [rows][ceil(K/32)] (weight rows in the
  * original order; act rows 0..M-1). */

@@ -70,6 +70,7 @@ def test_act_bind_layout(L):
 def _calls(L, a, w):
     yield L.svdq_mx_quantize_act(P, 520, ctypes.byref(w), ctypes.byref(a), None)
     yield L.svdq_mx_gemm(ctypes.byref(a), ctypes.byref(w), None, 0, P, 1000, 0, None)
+    yield L.svdq_mx_linear(P, 520, ctypes.byref(w), ctypes.byref(a), None, 0, P, 1000, 0, None)
 
 
 @pytest.mark.parametrize("field,value", [("n_tile", 384), ("N_pad", 1000), ("K_pad", 520), ("N", 1001), ("r", 8),
@@ -80,7 +81,7 @@ def test_weight_descriptors_refused(L, field, value):
     setattr(w, field, value)
     if field == "r":
         a.r = value
-    assert list(_calls(L, a, w)) == [1, 1]
+    assert list(_calls(L, a, w)) == [1, 1, 1]
     assert L.svdq_mx_export_weight(ctypes.byref(w), P, P, None) == 1
     assert b"descriptor" in L.svdq_last_error()
 
@@ -90,7 +91,7 @@ def test_weight_descriptors_refused(L, field, value):
 def test_act_descriptors_refused(L, field, value):
     a, w = _pair(L)
     setattr(a, field, value)
-    assert list(_calls(L, a, w)) == [1, 1]
+    assert list(_calls(L, a, w)) == [1, 1, 1]
     assert L.svdq_mx_export_act(ctypes.byref(a), P, P, None) == 1
     assert L.svdq_mx_dequantize_act(ctypes.byref(a), P, 520, 0, None) == 1
 
@@ -111,6 +112,11 @@ def test_call_arguments_refused(L):
     assert L.svdq_mx_gemm(A, W, None, 0, P, 1004, 0, None) == 2     # rows of bf16 off 16 bytes
     assert L.svdq_mx_gemm(A, W, None, 0, odd, 1000, 0, None) == 2
     assert L.svdq_mx_gemm(A, W, odd, 1, P, 1000, 0, None) == 2
+    # the whole layer refuses what either part refuses
+    assert L.svdq_mx_linear(None, 520, W, A, None, 0, P, 1000, 0, None) == 1
+    assert L.svdq_mx_linear(P, 524, W, A, None, 0, P, 1000, 0, None) == 2
+    assert L.svdq_mx_linear(P, 520, W, A, None, 1, P, 1000, 0, None) == 1
+    assert L.svdq_mx_linear(P, 520, W, A, None, 0, P, 1004, 0, None) == 2
     assert L.svdq_mx_dequantize_act(A, odd, 520, 0, None) == 2
     assert L.svdq_mx_dequantize_act(A, P, 512, 0, None) == 2
     assert L.svdq_mx_dequantize_act(A, P, 520, 7, None) == 1
@@ -118,7 +124,7 @@ def test_call_arguments_refused(L):
     a2, _ = _pair(L, r=32)
     assert L.svdq_mx_gemm(ctypes.byref(a2), W, None, 0, P, 1000, 0, None) == 1
     if not torch.cuda.is_available():                               # well-formed: stops at the device
-        assert list(_calls(L, a, w)) == [3, 3]
+        assert list(_calls(L, a, w)) == [3, 3, 3]
 
 
 def test_pack_and_bind_arguments_refused(L):
