@@ -1549,17 +1549,18 @@ int mx_n_pad(int N, int swiglu) {
 
 // Where the few-row kernels run (measured on B200 with weights from HBM; quantizer, product in us).
 // The quantizer up to 384 rows with a branch (every group of 8 rows reads L1s^T again), up to 1024 without:
-// K = 3072, r = 32: 4.2 (one row) to 8.6 (384) against kernel 1's 11.1, 14.9 / 11.1 at 512; K = 12288, r = 32:
-// 8.1 to 24.1 against 27.2, 41 / 27 at 512; K = 1024, r = 32: 5.6 / 7.0 at 384; K = 3072, r = 0: 1.5 to 4.3 against
-// 6.4, 7.2 / 6.6 at 2048; K = 1024, r = 0: 3.0 / 3.6 at 1024, 3.9 / 3.6 at 1536.
-// The product up to 48 rows, and up to 128 where K covers the wider epilogue: 3072 -> 9216 9.9 against the
-// pair GEMM's 11.3 at 40 rows, 11.6 / 11.8 at 96, 12.7 / 12.0 at 128; 12288 -> 3072 11.1 / 27.0 at one
-// row, 14.1 / 27.8 at 128; 256 -> 9216 5.2 / 5.6 at 40, 6.2 / 5.8 at 64, 8.9 / 6.2 at 128.
+// K = 3072, r = 32: 3.9 (one row) to 8.6 (384) against kernel 1's 11.0, 14.9 / 11.1 at 512; K = 12288, r = 32:
+// 7.8 to 24.1 against 26.3, 41 / 27 at 512; K = 1024, r = 32: 5.6 / 7.0 at 384; K = 3072, r = 0: 1.5 to 4.3 against
+// 6.9, 7.2 / 6.6 at 2048; K = 1024, r = 0: 3.0 / 3.6 at 1024, 3.9 / 3.6 at 1536.
+// The product up to 32 rows, and up to 128 where splitting K over the SMs outweighs its epilogue of M x N sums:
+// 3072 -> 9216 7.7 against the pair GEMM's 9.3 at one row, 9.1 / 9.4 at 40, 10.0 / 9.5 at 64; 3072 -> 3072 6.9 / 8.3
+// at 64, 8.4 / 8.5 at 128; 12288 -> 3072 10.2 / 21.3 at one row, 13.3 / 21.7 at 128; 256 -> 9216 4.0 / 4.9 at 16,
+// 5.4 / 5.0 at 40; 3072 -> 24576 with SwiGLU 12.8 / 16.2 at one row, 16.3 / 16.4 at 64.
 bool mx_few_quant_rows(int M, int K_pad, int r) {
   return r == 0 ? M <= 1024 : M <= 384 && K_pad <= kFewQuantMaxK;
 }
-bool mx_few_product_rows(int M, int K_pad) {
-  return M <= 48 || (M <= svdq::mx::kFewCols && K_pad >= 32 * M);
+bool mx_few_product_rows(int M, int K_pad, int N) {
+  return M <= 32 || (M <= svdq::mx::kFewCols && 128ll * K_pad >= 1ll * M * N);
 }
 
 struct MxWeightLayout {
@@ -1979,7 +1980,7 @@ svdq_status mx_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const uint1
   int dev, sms;
   if (svdq_status s = mx_ready(&dev, &sms); s != SVDQ_OK) return s;
 
-  if (mx_few_product_rows(act->M, act->K_pad)) {
+  if (mx_few_product_rows(act->M, act->K_pad, w->N)) {
     bool done = false;
     if (svdq_status s = mx_few_gemm(act, w, bias, has_bias, swiglu, Y, ldy, esize, dev, stream, &done);
         s != SVDQ_OK || done)
