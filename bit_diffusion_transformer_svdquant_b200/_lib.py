@@ -744,10 +744,10 @@ def _norm_rows(t, name, shape=None, device=None):
     if D > 1 and st[-1] != 1:
         raise ValueError(f"{name}: rows must be contiguous, got strides {st}")
     ld = st[-2] if T > 1 else D
-    ss = st[0] if len(sh) == 3 and sh[0] > 1 else 0
-    if ld < D or (ss and ss < (T - 1) * ld + D):
+    many = len(sh) == 3 and sh[0] > 1
+    if ld < D or (many and st[0] < (T - 1) * ld + D):
         raise ValueError(f"{name}: rows overlap (strides {st})")
-    return t.data_ptr(), ld, f32, 0 if ss == T * ld else ss
+    return t.data_ptr(), ld, f32, st[0] if many and st[0] != T * ld else 0
 
 
 def _mod(m, name, D, samples, device, f32):

@@ -247,6 +247,38 @@ def test_binding_refuses_before_the_library(L):
         svdq.MxWeight.from_state({**state, "format": None, "blob": None}, "cpu")
 
 
+class _AsIfOnDevice:
+    """A CPU tensor's shape, strides and address, as the binding reads them of a device tensor."""
+    is_cuda = True
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+@pytest.mark.parametrize("make", [
+    lambda: torch.zeros(1, 6, 64).expand(3, 6, 64),                    # one sample standing for three
+    lambda: torch.zeros(1, 1, 64).expand(3, 1, 64),
+    lambda: torch.zeros(3, 1, 64).expand(3, 6, 64),
+    lambda: torch.zeros(1, 64).expand(6, 64),
+    lambda: torch.zeros(4096).as_strided((3, 6, 64), (320, 64, 1)),    # a sample's last row is the next one's first
+    lambda: torch.zeros(4096).as_strided((6, 64), (32, 1)),
+])
+def test_rows_that_share_memory_are_refused(make):
+    with pytest.raises(ValueError, match="overlap"):
+        svdq._lib._norm_rows(_AsIfOnDevice(make()), "x")
+
+
+@pytest.mark.parametrize("shape,strides,ld,sample", [
+    ((3, 6, 64), (384, 64, 1), 64, 0), ((3, 6, 64), (768, 128, 1), 128, 0), ((3, 6, 64), (1000, 64, 1), 64, 1000),
+    ((3, 1, 64), (100, 7, 1), 64, 100), ((1, 6, 64), (0, 80, 1), 80, 0), ((3, 1, 64), (64, 0, 1), 64, 0)])
+def test_row_and_sample_strides(shape, strides, ld, sample):
+    t = torch.zeros(4096).as_strided(shape, strides)
+    assert svdq._lib._norm_rows(_AsIfOnDevice(t), "x") == (t.data_ptr(), ld, 1, sample)
+
+
 C_PROGRAM = r"""
 #include <stddef.h>
 #include <stdio.h>
