@@ -712,6 +712,10 @@ class Norm:
         if not eps >= 0.0:
             raise ValueError(f"eps {eps}: expected a non-negative number")
         self.kind, self.eps, self.weight, self.bias = kind, float(eps), weight, bias
+        self._check()
+
+    def _check(self):
+        weight, bias = self.weight, self.bias
         self.D = self.device = None
         given = [v for v in (weight, bias) if v is not None]
         for v in given:
@@ -721,9 +725,20 @@ class Norm:
         if given:
             self.D, self.device = given[0].shape[0], given[0].device
             _same_device(self.device, weight=weight, bias=bias)
-        # the fields of svdq_norm
-        self.fields = (NORM_KINDS[kind], self.eps, int(bool(given) and given[0].dtype == torch.float32), 0,
-                       0 if weight is None else weight.data_ptr(), 0 if bias is None else bias.data_ptr())
+        self._f32 = int(bool(given) and given[0].dtype == torch.float32)
+        self._checked, self._pointers = (weight, bias), self._addresses()
+
+    def _addresses(self):
+        return (0 if self.weight is None else self.weight.data_ptr(), 0 if self.bias is None else self.bias.data_ptr())
+
+    def fields(self, name, D, device):
+        """The fields of svdq_norm for rows of D on `device`; vectors that were exchanged are checked again."""
+        if self._checked[0] is not self.weight or self._checked[1] is not self.bias \
+                or self._pointers != self._addresses():
+            self._check()
+        if self.D is not None and (self.D != D or self.device != device):
+            raise ValueError(f"{name}: vectors of {self.D} on {self.device}, expected {D} on {device}")
+        return (NORM_KINDS[self.kind], self.eps, self._f32, 0, *self._pointers)
 
 
 _F32 = {torch.bfloat16: 0, torch.float32: 1}
@@ -787,9 +802,8 @@ def _norm_args(x, y, gate, post, res_scale, skip_scale, norm, scale, shift, offs
     p_gate, ld_gate = _mod(gate, "gate", D, samples, device, mod_f32)
     p_scale, ld_scale = _mod(scale, "scale", D, samples, device, mod_f32)
     p_shift, ld_shift = _mod(shift, "shift", D, samples, device, mod_f32)
-    for name, n in (("post", post), ("norm", norm)):
-        if n is not None and n.D is not None and (n.D != D or n.device != device):
-            raise ValueError(f"{name}: vectors of {n.D} on {n.device}, expected {D} on {device}")
+    post_fields = _NO_NORM if post is None else post.fields("post", D, device)
+    norm_fields = _NO_NORM if norm is None else norm.fields("norm", D, device)
     py, ldy, y_f32, sy, po, ldo, so = 0, 0, 0, 0, 0, 0, 0
     if y is not None:
         py, ldy, y_f32, sy = _norm_rows(y, "y", shape, device)
@@ -801,7 +815,7 @@ def _norm_args(x, y, gate, post, res_scale, skip_scale, norm, scale, shift, offs
         return None  # no row: empty tensors have no address to pass
     return _PACK_NORM_ARGS(M, D, samples, T, p_off, px, ldx, x_f32, y_f32, py, ldy, po, ldo, ph, ldh, h_f32, mod_f32,
                            p_gate, ld_gate, p_scale, ld_scale, p_shift, ld_shift, skip_scale, res_scale,
-                           *(_NO_NORM if post is None else post.fields), *(_NO_NORM if norm is None else norm.fields), sx, sy, so, sh)
+                           *post_fields, *norm_fields, sx, sy, so, sh)
 
 
 def _run_norm(a, device, w=None, act=None):
@@ -886,7 +900,7 @@ def mlp_mx(x, w_up: MxWeight, w_down: MxWeight, bias_up=None, bias_down=None, no
         raise ValueError(f"w_down returns {w_down.N} values to a residual stream of {x.shape[-1]}")
     rows = x.shape[:-1].numel()
     if rows == 0:
-        return _like(x, None) if norm is not None else x.new_empty((0, w_down.N))
+        return out if out is not None else _like(x, None) if norm is not None else x.new_empty((0, w_down.N))
     act_up, act_down = acts or (MxAct(rows, w_up.K, w_up.r, x.device), MxAct(rows, w_down.K, w_down.r, x.device))
     if norm is None:
         quantize_act_mx(x, w_up, act_up)

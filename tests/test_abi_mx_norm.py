@@ -279,6 +279,24 @@ def test_row_and_sample_strides(shape, strides, ld, sample):
     assert svdq._lib._norm_rows(_AsIfOnDevice(t), "x") == (t.data_ptr(), ld, 1, sample)
 
 
+def test_a_norm_follows_its_vectors():
+    def vector(*shape, dtype=torch.float32):
+        return _AsIfOnDevice(torch.ones(*shape, dtype=dtype))
+    n = svdq.Norm("layer", vector(64), vector(64))
+    device = n.weight.device
+    assert n.fields("norm", 64, device)[2:] == (1, 0, n.weight.data_ptr(), n.bias.data_ptr())
+    n.weight, n.bias = vector(128, dtype=torch.bfloat16), None              # other vectors
+    assert n.fields("norm", 128, device)[2:] == (0, 0, n.weight.data_ptr(), 0)
+    n.weight.t.data = torch.ones(128, dtype=torch.bfloat16)                 # the same tensor, other memory
+    assert n.fields("norm", 128, device)[4] == n.weight.t.data_ptr()
+    n.weight.t.data = torch.ones(32, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="vectors of 32"):
+        n.fields("norm", 128, device)
+    n.bias = vector(16, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="of one type"):
+        n.fields("norm", 32, device)
+
+
 C_PROGRAM = r"""
 #include <stddef.h>
 #include <stdio.h>
