@@ -2370,10 +2370,13 @@ svdq_status run_norm(const svdq_block_norm_args* a, const svdq_mx_weight* w, con
     const auto stage_bytes = [&] { return norm_batch(chunks) * chunks * 256 * W * elem_bytes; };
     const auto factor_bytes = [&] { return chunks * 256 * W * (a->y ? 12 : 8); };
     const auto lambda_bytes = [&] { return act ? chunks * 256 * W * 4 : 0; };
-    // factors of a run's sample in shared memory where a run gives every group two batches; else (or
-    // where they do not fit beside a batch) two or eight chunks per thread and vectors read per row
+    // Factors of a run's sample in shared memory where a run gives every group two batches and the SMs have
+    // more than two rows each; else (or where they do not fit beside a batch) two or eight chunks per thread
+    // and vectors read per row, which with few rows is sooner done: 24 and 296 rows of 3072, gate, post-norm,
+    // residual and norm 6.4 and 6.9 us against 7.2 with shared factors, quantized 7.5 against 9.0 (24 rows),
+    // a norm alone 3.7 against 4.9; at 400 rows 7.6 / 7.3 and 4.5 / 5.1, at 600 rows 10.4 / 7.4 and 5.7 / 5.2.
     const int per_run = a->offsets ? a->M / a->samples : a->rows_per_sample;
-    const bool share = per_run >= 2 * (svdq::norm::kMaxWarps / W) * norm_batch(chunks) &&
+    const bool share = a->M > 2 * sms && per_run >= 2 * (svdq::norm::kMaxWarps / W) * norm_batch(chunks) &&
                        stage_bytes() + factor_bytes() + lambda_bytes() <= kNormSmem;
     if (!share) {
       W = row_warps(2);
@@ -2388,14 +2391,16 @@ svdq_status run_norm(const svdq_block_norm_args* a, const svdq_mx_weight* w, con
       // A quantized output is bound by its instructions: more groups, up to 128 KB (16896 rows of 3072 with
       // y: 6 groups 91 us, 8 groups 79 us).
       // Two sets of factors where they cost no group.
-      const int in_flight = (act ? 128 : 80) * 1024, R = norm_batch(chunks);
+      const int in_flight = (act ? 128 : 80) * 1024, R = norm_batch(chunks), batches = (k.rows + R - 1) / R;
       int groups = svdq::norm::kMaxWarps / W, fixed = share ? factor_bytes() + lambda_bytes() : 0;
       while (groups > 1 && (groups * stage_bytes() > in_flight || groups * stage_bytes() + fixed > kNormSmem)) --groups;
+      if (!share)
+        while (groups > 1 && (groups - 1) * sms >= batches) --groups;  // few rows: over all SMs
       const int sets = share && groups * stage_bytes() + fixed + factor_bytes() <= kNormSmem ? 2 : 1;
       if (sets == 2) fixed += factor_bytes();
       const int stages =
           2 * groups * stage_bytes() <= 80 * 1024 && 2 * groups * stage_bytes() + fixed <= kNormSmem ? 2 : 1;
-      const int batches = (k.rows + R - 1) / R, blocks = (batches + groups - 1) / groups;
+      const int blocks = (batches + groups - 1) / groups;
       cfg.gridDim = dim3(blocks < sms ? blocks : sms, 1, 1);
       cfg.blockDim = dim3(groups * 32 * W, 1, 1);
       cfg.dynamicSmemBytes = static_cast<size_t>(groups) * stages * stage_bytes() + fixed;

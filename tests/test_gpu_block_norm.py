@@ -128,6 +128,46 @@ def test_gated_residual(cuda_device, B, T, D, post, kind):
             _check(got_h.reshape(-1, D), h, he, ht, f"h {xt}")
 
 
+# rows enough for the factors of a sample to be shared: every chunk width, runs of several samples
+MANY_ROWS = [(1, 400, 256), (3, 110, 512), (1, 310, 768), (2, 200, 1000), (1, 330, 1536), (3, 150, 1544), (2, 160, 3072),
+             (1, 310, 8192), (1, 300, 16384), (1, 299, 32768)]
+
+
+@pytest.mark.parametrize("B,T,D", MANY_ROWS)
+def test_many_rows(cuda_device, B, T, D):
+    g = torch.Generator(device="cuda").manual_seed(B + T + 3 * D)
+    at = np.repeat(np.arange(B), T)
+    for xt, yt, post, kind in ((BF16, BF16, "rms", "layer"), (F32, BF16, "layer", "rms")):
+        x, y = _rand(g, B, T, D, dtype=xt, std=4.0), _rand(g, B, T, D, dtype=yt, std=2.0, mean=0.5)
+        gate, scale, shift = _rand(g, B, 3 * D, std=0.5).split(D, dim=1)
+        pn, nn = _norm(g, post, D, True), _norm(g, kind, D, False)
+        xo, e, h, he = _run(x, y, at, gate, pn, 1.0, 0.5, nn, scale, shift)
+        got_x, got_h = svdq.gated_residual(x, y, gate=gate, post=pn, res_scale=0.5, norm=nn, scale=scale, shift=shift)
+        _check(got_x.reshape(-1, D), xo, e, xt, f"x' {xt}")
+        _check(got_h.reshape(-1, D), h, he, BF16, f"h {xt}")
+        _, _, h, he = _run(x, None, at, norm=nn, scale=scale, shift=shift)
+        _check(svdq.block_norm(x, nn, scale, shift).reshape(-1, D), h, he, xt, f"norm {xt}")
+
+
+@pytest.mark.parametrize("lengths", [[100, 0, 57, 1, 300], [31, 33, 350], [0, 460], [9] * 50])
+def test_many_packed_rows(cuda_device, lengths):
+    g = torch.Generator(device="cuda").manual_seed(len(lengths))
+    lead, tail, D = 2, 7, 1544
+    offsets = [lead + sum(lengths[:i]) for i in range(len(lengths) + 1)]
+    M, B = offsets[-1] + tail, len(lengths)
+    at = ref.sample_rows(offsets, M)
+    x, y = _rand(g, M, D, dtype=F32), _rand(g, M, D)
+    gate, scale, shift = _rand(g, B, 3 * D, std=0.5).split(D, dim=1)
+    norm, inside = _norm(g, "layer", D, True), at >= 0
+    out, h = torch.full_like(x, 7.0), torch.full_like(y, 7.0)
+    packed = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    svdq.gated_residual(x, y, gate=gate, norm=norm, scale=scale, shift=shift, out=out, h=h, offsets=packed)
+    xo, e, hw, he = _run(x[inside], y[inside], at[inside], gate, norm=norm, scale=scale, shift=shift)
+    _check(out[inside], xo, e, F32, "x'")
+    _check(h[inside], hw, he, BF16, "h")
+    assert (out[~inside] == 7.0).all() and (h[~inside] == 7.0).all()
+
+
 def test_plain_residual_in_place(cuda_device):
     g = torch.Generator(device="cuda").manual_seed(1)
     for D in (96, 97):
@@ -249,7 +289,8 @@ def _mx_weight(g, N, K):
 
 
 @pytest.mark.parametrize("B,T,D", [(1, 1, 8), (2, 3, 40), (1, 130, 264), (3, 50, 1544), (1, 300, 3072), (2, 9, 8192),
-                                   (1, 2, 32768)])
+                                   (1, 2, 32768), (1, 290, 1032), (1, 297, 1032), (2, 160, 264), (3, 110, 512),
+                                   (1, 320, 8192)])
 def test_quantized_is_the_unfused_chain(cuda_device, B, T, D):
     g = torch.Generator(device="cuda").manual_seed(B + T + D)
     x, y = _rand(g, B, T, D, std=3.0), _rand(g, B, T, D)
