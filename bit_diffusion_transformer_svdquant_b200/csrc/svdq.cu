@@ -2388,10 +2388,16 @@ svdq_status run_norm(const svdq_block_norm_args* a, const svdq_mx_weight* w, con
       // 3072, all bf16 (12 KB of x and y): 6 groups 137 us, 8 groups 157 us, 4 groups 171 us, 6 groups with
       // two stages 138 us; without y (6 KB) over 4608 rows: 8 groups 13.2 us, 6 groups 15.2 us, 8 groups with
       // two stages 13.9 us; 4000 rows of 8192 without y (2 groups, 32 KB): one stage 33.8 us, two 32.1 us.
-      // A quantized output is bound by its instructions: more groups, up to 128 KB (16896 rows of 3072 with
-      // y: 6 groups 91 us, 8 groups 79 us).
+      // More groups, up to 128 KB, for a quantized output, which is bound by its instructions (16896 rows of
+      // 3072 with y: 6 groups 91 us, 8 groups 79 us), and where the call's bytes about fit the L2, so that the
+      // rounds of rows count, and rows fill the groups (with y, bf16, from HBM: 1000 rows 11.0 -> 9.8 us, 4608
+      // 27.8 -> 25.5, 6000 32.8 / 32.8; x fp32: 3000 29.2 -> 27.3, 4608 37.5 / 37.6, 8448 60.5 / 66.6; bf16 from
+      // L2, 600 rows 7.5 / 8.3).
       // Two sets of factors where they cost no group.
-      const int in_flight = (act ? 128 : 80) * 1024, R = norm_batch(chunks), batches = (k.rows + R - 1) / R;
+      const long long bytes = 1ll * a->M * a->D * (elem_bytes + (a->x_out == nullptr ? 0 : a->x_f32 ? 4 : 2) +
+                                                   (a->h == nullptr ? 0 : a->h_f32 ? 4 : 2));
+      const bool more = act || (bytes <= 160ll * 1000 * 1000 && a->M > 6 * sms);
+      const int in_flight = (more ? 128 : 80) * 1024, R = norm_batch(chunks), batches = (k.rows + R - 1) / R;
       int groups = svdq::norm::kMaxWarps / W, fixed = share ? factor_bytes() + lambda_bytes() : 0;
       while (groups > 1 && (groups * stage_bytes() > in_flight || groups * stage_bytes() + fixed > kNormSmem)) --groups;
       if (!share)
