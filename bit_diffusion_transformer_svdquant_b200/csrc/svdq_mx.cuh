@@ -111,6 +111,8 @@ struct ActArgs {
 // block each; the lane beside it (lane ^ 1) holds the other half, and the four lanes of a row the
 // stage's two blocks, whose scales lane b = 0 stores together. Reading X bounds the kernel, as for
 // NVFP4 (the same ring, TMA stages and branch MMAs); the scale costs one shift per block there.
+// Measured on B200: 4608 rows of 12288, r = 0, 26.7 us (5.5 TB/s of X, codes and scales), 16896 rows of 3072, r = 32,
+// 27 us (5.0 TB/s).
 struct Act {
   using Args = ActArgs;
   __device__ static void prologue(const Args&, float*) {}
@@ -201,6 +203,8 @@ struct GemmArgs {
 };
 
 // The MXFP4 format of the pair GEMM. A K step's two scale atoms each serve two MMAs (data ids 0 and 2).
+// Operands between L2 and the SMs bound it, as for NVFP4, with half the scale bytes: 16896 x 3072 x 9216, r = 32,
+// 194-203 us on B200 (4.8-5.0 PFLOP/s), 4608 x 3072 x 24576 with SwiGLU and bias 160-166 us.
 struct Gemm {
   using Args = GemmArgs;
   static constexpr bool kScales = true;
@@ -355,7 +359,8 @@ __device__ __forceinline__ float2 e2m1x2_value(uint32_t byte) {
 }
 
 // The values of a quantized activation: dec(q) 2^e, exact in fp32. A thread takes 8 columns of kDeqRows
-// rows, whose loads go out together; writing the values bounds it.
+// rows, whose loads go out together; writing the values bounds it (4608 rows of 12288 to bf16 in 25.2 us, 5.8 TB/s;
+// one row per thread 33 us).
 constexpr int kDeqRows = 4;
 template <bool F32>
 __global__ void __launch_bounds__(256) dequantize_act_kernel(const uint8_t* __restrict__ codes,

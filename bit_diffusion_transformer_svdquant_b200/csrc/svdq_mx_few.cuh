@@ -9,6 +9,10 @@
 //
 // The quantizer for few rows splits K over clusters too: a row's 32-element blocks are independent, and
 // the down-projection's partial sums meet at the cluster's first CTA, in a fixed order.
+//
+// Measured on B200 for one token of 3072 -> 9216, r = 32, weight from HBM: quantizer 3.9 us, product 7.7 us (2.0 TB/s),
+// the layer 11.8 us; for kernel 1 and the pair GEMM 11.0 and 9.3 us. Launch, cluster set-up, the first loads and the
+// exchange of the sums come one after another and bound both.
 #pragma once
 #include <cstdint>
 #include <cuda.h>

