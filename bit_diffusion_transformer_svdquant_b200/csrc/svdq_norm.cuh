@@ -376,7 +376,7 @@ __device__ __forceinline__ Run run_at(const Args& a, int m, int limit) {
     // rows per sample come with the run: the sample's end is the first row of the next
     if (r.s >= 0) r.end = min(limit, min(a.M, (r.s + 1) * a.rows_per_sample));
   } else if (r.s >= 0) {
-    r.end = min(limit, __ldg(a.offsets + r.s + 1));
+    r.end = min(min(limit, a.M), __ldg(a.offsets + r.s + 1));  // a quantized output has rows of padding behind M
   } else if (m < __ldg(a.offsets)) {
     r.end = min(limit, __ldg(a.offsets));
   }

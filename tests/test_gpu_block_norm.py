@@ -448,3 +448,25 @@ def test_slices_of_a_joint_stream(cuda_device):
     # samples in another order than memory's are refused, not misread
     with pytest.raises(ValueError, match="overlap"):
         svdq.block_norm(both.transpose(0, 1), svdq.Norm("rms"))
+
+
+def test_quantized_offsets_past_the_rows(cuda_device):
+    """Offsets that reach behind the last row: the rows of padding of a quantized output are zero, not read
+    from behind x, and x' ends with its rows. Tensors lie inside larger ones."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    M, D = 40, 256
+    whole_x, whole_y = _rand(g, 400, D, dtype=F32), _rand(g, 400, D)
+    x, y, w = whole_x[:M], whole_y[:M], _mx_weight(g, 128, D)
+    norm = svdq.Norm("rms")
+    for last in (M, M + 20, 128, 1 << 30, 2 ** 31 - 1):
+        offsets = torch.tensor([0, 12, last], dtype=torch.int32, device="cuda")
+        out, act = torch.full_like(whole_x, 7.0), svdq.MxAct(M, D, 0, "cuda")
+        act.buf.fill_(0xA5)
+        svdq.gated_residual_quantize_mx(x, y, norm, w, act, offsets=offsets, out=out[:M])
+        want = svdq.gated_residual(x, y, norm=norm, offsets=torch.tensor([0, 12, M], dtype=torch.int32, device="cuda"))
+        assert torch.equal(out[:M], want[0]) and (out[M:] == 7.0).all()
+        codes = act.buf[:act.desc.M_pad * act.desc.K_pad // 2].view(act.desc.M_pad, -1)
+        assert (codes[M:] == 0).all()
+        ref_act = svdq.quantize_act_mx(want[1], w, svdq.MxAct(M, D, 0, "cuda"))
+        for u, v in zip(svdq.export_act_mx(act), svdq.export_act_mx(ref_act)):
+            assert torch.equal(u, v)
