@@ -2142,9 +2142,10 @@ bool misaligned(const void* p, int f32) { return (reinterpret_cast<uintptr_t>(p)
 struct Span {
   uintptr_t lo, hi;
   uintptr_t row, ls, block, ss;
+  bool even;  // one run of rows, ls apart throughout
   Span(const void* p, const svdq_block_norm_args* a, long long ld, long long sample, int f32) {
     const uintptr_t e = f32 ? 4 : 2;
-    const bool even = a->offsets != nullptr || sample == 0 || a->M <= a->rows_per_sample;
+    even = a->offsets != nullptr || sample == 0 || a->M <= a->rows_per_sample;
     const long long rows = even ? a->M : a->rows_per_sample, samples = even ? 1 : (a->M + rows - 1) / rows;
     row = a->D * e;
     ls = ld * e;
@@ -2161,8 +2162,7 @@ struct Span {
       const uintptr_t d = q >= p ? (q - p) % period : (period - (p - q) % period) % period;
       return d >= n && d + m <= period;
     };
-    if (ls == o.ls && (ss == block || ss % ls == 0) && (o.ss == o.block || o.ss % ls == 0) &&
-        beside(lo, row, o.lo, o.row, ls))
+    if (ls == o.ls && (even || ss % ls == 0) && (o.even || o.ss % ls == 0) && beside(lo, row, o.lo, o.row, ls))
       return false;
     return !(ss == o.ss && ss > block && beside(lo, block, o.lo, o.block, ss));
   }

@@ -193,6 +193,32 @@ def test_block_norm_well_formed(L, change):
     assert L.svdq_block_norm(ctypes.byref(_norm_args(**change)), None) == 3, L.svdq_last_error()
 
 
+# Samples whose stride is exactly the bytes they span, (rows - 1) ld + D: the columns of the next sample lie D further
+# on, so that what is beside x in one sample is x itself in the next.
+CLOSE = dict(sx=5 * 80 + 40, ldx=80, y=None, gate=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(CLOSE, x_out=None, h=BASE + 80, ldh=80, sh=440),
+    dict(CLOSE, x_out=None, h=BASE + 80, ldh=80),                       # an even output beside it
+    dict(CLOSE, x_out=None, h=BASE + 80, ldh=80, sh=480),
+    dict(x_out=BASE + 80, s_out=440, ld_out=80, sx=440, ldx=80),
+    dict(samples=12, rows_per_sample=1, sx=40, ldx=80, x_out=BASE + 80, s_out=40, ld_out=80),
+    dict(y=BASE + 80, sy=440, ldy=80, x_out=BASE, s_out=440, ld_out=80),
+])
+def test_samples_that_touch_are_not_beside_each_other(L, change):
+    assert L.svdq_block_norm(ctypes.byref(_norm_args(**change)), None) == 1, L.svdq_last_error()
+    assert b"overlaps" in L.svdq_last_error()
+
+
+@pytest.mark.parametrize("change", [dict(sx=480, ldx=80, sh=480, ldh=80, h=BASE + 80), dict(ldx=80, ldh=80, h=BASE + 80),
+                                    dict(sx=440, ldx=80), dict(sx=440, ldx=80, s_out=440, ld_out=80, x_out=BASE)])
+def test_samples_apart_or_in_place_are_taken(L, change):
+    if torch.cuda.is_available():
+        pytest.skip("fake addresses: CPU only")
+    assert L.svdq_block_norm(ctypes.byref(_norm_args(**change)), None) == 3, L.svdq_last_error()
+
+
 def _quant_pair(L, r=0):
     act, w = _pair(L, M=12, K=40, N=1000, r=r)
     w.K_pad = 256
