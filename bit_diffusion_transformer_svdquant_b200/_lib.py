@@ -818,14 +818,16 @@ def _norm_args(x, y, gate, post, res_scale, skip_scale, norm, scale, shift, offs
                            *post_fields, *norm_fields, sx, sy, so, sh)
 
 
-def _run_norm(a, device, w=None, act=None):
-    if a is None:
-        return
-    if act is None:
+def _run_norm(a, device):
+    if a is not None:
         _enqueue(device, ("svdq_block_norm", a))
-    else:
-        _same_device(device, weight=w, act=act)
-        _enqueue(device, ("svdq_block_norm_quantize_mx", a, byref(w.desc), byref(act.desc)))
+
+
+def _run_norm_quantize(a, x, w, act):
+    if a is None:  # an activation has a row at least: it would keep what it held
+        raise ValueError(f"act holds {act.M} rows, x none")
+    _same_device(x.device, weight=w, act=act)
+    _enqueue(x.device, ("svdq_block_norm_quantize_mx", a, byref(w.desc), byref(act.desc)))
 
 
 def _like(x, dtype):
@@ -866,7 +868,7 @@ def gated_residual(x, y, gate=None, post: Norm | None = None, res_scale: float =
 def norm_quantize_act_mx(x, norm: Norm, w: MxWeight, act: MxAct, scale=None, shift=None, offsets=None) -> MxAct:
     """block_norm whose bf16 result is quantized for the next layer instead of stored: the codes and
     scales quantize_act_mx makes of it. For weights without a branch."""
-    _run_norm(_norm_args(x, None, None, None, 1.0, 1.0, norm, scale, shift, offsets, None, None), x.device, w, act)
+    _run_norm_quantize(_norm_args(x, None, None, None, 1.0, 1.0, norm, scale, shift, offsets, None, None), x, w, act)
     return act
 
 
@@ -876,8 +878,8 @@ def gated_residual_quantize_mx(x, y, norm: Norm, w: MxWeight, act: MxAct, gate=N
     """gated_residual with norm whose bf16 h is quantized for the next layer instead of stored. Returns
     (x', act). For weights without a branch."""
     out = _like(x, None) if out is None else out
-    _run_norm(_norm_args(x, y, gate, post, res_scale, skip_scale, norm, scale, shift, offsets, out, None), x.device, w,
-              act)
+    _run_norm_quantize(_norm_args(x, y, gate, post, res_scale, skip_scale, norm, scale, shift, offsets, out, None), x, w,
+                       act)
     return out, act
 
 

@@ -305,6 +305,18 @@ def test_row_and_sample_strides(shape, strides, ld, sample):
     assert svdq._lib._norm_rows(_AsIfOnDevice(t), "x") == (t.data_ptr(), ld, 1, sample)
 
 
+def test_no_rows_to_quantize_are_refused():
+    """An empty x leaves nothing to write into an activation of at least one row, whose codes of the call before
+    would pass for its own."""
+    class Act:
+        M = 4
+    x = _AsIfOnDevice(torch.empty(0, 64))
+    with pytest.raises(ValueError, match="act holds 4 rows, x none"):
+        svdq.norm_quantize_act_mx(x, svdq.Norm("rms"), None, Act)
+    with pytest.raises(ValueError, match="act holds 4 rows, x none"):
+        svdq.gated_residual_quantize_mx(x, x, svdq.Norm("rms"), None, Act, out=x)
+
+
 def test_a_norm_follows_its_vectors():
     def vector(*shape, dtype=torch.float32):
         return _AsIfOnDevice(torch.ones(*shape, dtype=dtype))
