@@ -2277,6 +2277,14 @@ NormKernel norm_kernel(int chunks, bool share, bool x_f32, int y, bool quant) {
   if (quant) return x_f32 ? norm_kernel<true, true>(chunks, share, y) : norm_kernel<false, true>(chunks, share, y);
   return x_f32 ? norm_kernel<true, false>(chunks, share, y) : norm_kernel<false, false>(chunks, share, y);
 }
+// Quantized forms whose shared factors leave no room for the smoothing reciprocals: rows of bf16 x and y in
+// (8192, 12288], rows of x alone in (12288, 16384].
+NormKernel norm_kernel_far_lambdas(bool x_f32, int y) {
+  using namespace svdq::norm;
+  if (y != kNoY) return block_norm_kernel<6, norm_batch(6), false, kBf16Y, true, true, false>;
+  return x_f32 ? block_norm_kernel<4, norm_batch(4), true, kNoY, true, true, false>
+               : block_norm_kernel<4, norm_batch(4), false, kNoY, true, true, false>;
+}
 cudaError_t launch_norm_any(const cudaLaunchConfig_t& cfg, int chunks, const svdq::norm::Args& k, int G) {
   switch (chunks) {
     case 1: return cudaLaunchKernelEx(&cfg, svdq::norm::block_norm_any_kernel<1>, k, G);
@@ -2298,6 +2306,9 @@ svdq_status norm_setup() {
     for (int v = 0; v < 24; ++v)
       SVDQ_CUDA(cudaFuncSetAttribute(norm_kernel(chunks, v >= 12, v & 1, (v >> 1) % 3, (v / 6) & 1),
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem));
+  for (int v = 0; v < 3; ++v)
+    SVDQ_CUDA(cudaFuncSetAttribute(norm_kernel_far_lambdas(v == 1, v == 2 ? svdq::norm::kBf16Y : svdq::norm::kNoY),
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem));
   return SVDQ_OK;
 }
 svdq_status norm_ready(int* sm_out) {
@@ -2369,7 +2380,6 @@ svdq_status run_norm(const svdq_block_norm_args* a, const svdq_mx_weight* w, con
   if (vec) {
     const auto stage_bytes = [&] { return norm_batch(chunks) * chunks * 256 * W * elem_bytes; };
     const auto factor_bytes = [&] { return chunks * 256 * W * (a->y ? 12 : 8); };
-    const auto lambda_bytes = [&] { return act ? chunks * 256 * W * 4 : 0; };
     // Factors of a run's sample in shared memory where a run gives every group two batches and the SMs have
     // more than two rows each; else (or where they do not fit beside a batch) two or eight chunks per thread
     // and vectors read per row, which with few rows is sooner done: 24 and 296 rows of 3072, gate, post-norm,
@@ -2377,7 +2387,11 @@ svdq_status run_norm(const svdq_block_norm_args* a, const svdq_mx_weight* w, con
     // a norm alone 3.7 against 4.9; at 400 rows 7.6 / 7.3 and 4.5 / 5.1, at 600 rows 10.4 / 7.4 and 5.7 / 5.2.
     const int per_run = a->offsets ? a->M / a->samples : a->rows_per_sample;
     const bool share = a->M > 2 * sms && per_run >= 2 * (svdq::norm::kMaxWarps / W) * norm_batch(chunks) &&
-                       stage_bytes() + factor_bytes() + lambda_bytes() <= kNormSmem;
+                       stage_bytes() + factor_bytes() <= kNormSmem;
+    // a quantized output's smoothing reciprocals, where the shared factors leave room for them
+    int lambda_bytes = act && share ? chunks * 256 * W * 4 : 0;
+    const bool far_lambdas = act && share && stage_bytes() + factor_bytes() + lambda_bytes > kNormSmem;
+    if (far_lambdas) lambda_bytes = 0;
     if (!share) {
       W = row_warps(2);
       chunks = (eights + 32 * W - 1) / (32 * W) <= 2 ? 2 : 8;
@@ -2398,7 +2412,7 @@ svdq_status run_norm(const svdq_block_norm_args* a, const svdq_mx_weight* w, con
                                                    (a->h == nullptr ? 0 : a->h_f32 ? 4 : 2));
       const bool more = act || (bytes <= 160ll * 1000 * 1000 && a->M > 6 * sms);
       const int in_flight = (more ? 128 : 80) * 1024, R = norm_batch(chunks), batches = (k.rows + R - 1) / R;
-      int groups = svdq::norm::kMaxWarps / W, fixed = share ? factor_bytes() + lambda_bytes() : 0;
+      int groups = svdq::norm::kMaxWarps / W, fixed = share ? factor_bytes() + lambda_bytes : 0;
       while (groups > 1 && (groups * stage_bytes() > in_flight || groups * stage_bytes() + fixed > kNormSmem)) --groups;
       if (!share)
         while (groups > 1 && (groups - 1) * sms >= batches) --groups;  // few rows: over all SMs
@@ -2410,9 +2424,11 @@ svdq_status run_norm(const svdq_block_norm_args* a, const svdq_mx_weight* w, con
       cfg.gridDim = dim3(blocks < sms ? blocks : sms, 1, 1);
       cfg.blockDim = dim3(groups * 32 * W, 1, 1);
       cfg.dynamicSmemBytes = static_cast<size_t>(groups) * stages * stage_bytes() + fixed;
-      e = cudaLaunchKernelEx(
-          &cfg, norm_kernel(chunks, share, a->x_f32, a->y == nullptr ? svdq::norm::kNoY : 1 + a->y_f32, act != nullptr), k,
-          32 * W, stages, sets, g_wait_ns.load());
+      const int y = a->y == nullptr ? svdq::norm::kNoY : 1 + a->y_f32;
+      e = cudaLaunchKernelEx(&cfg,
+                             far_lambdas ? norm_kernel_far_lambdas(a->x_f32, y)
+                                         : norm_kernel(chunks, share, a->x_f32, y, act != nullptr),
+                             k, 32 * W, stages, sets, g_wait_ns.load());
       if (e != cudaSuccess)
         return fail(SVDQ_ERR_CUDA, "launch of norm::block_norm_kernel failed: %s", cudaGetErrorString(e));
       return check_launch("norm::block_norm_kernel");

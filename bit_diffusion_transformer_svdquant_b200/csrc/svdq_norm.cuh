@@ -394,13 +394,16 @@ __device__ __forceinline__ Run run_at(const Args& a, int m, int limit) {
 //   - SHARE: the factors of the run's sample are laid in shared memory once per run, because reading the
 //     vectors for every row came to twice the bytes of the row itself. Where runs are too short for that
 //     (or rows too long) every row reads them from global memory.
+//     A quantized output's smoothing reciprocals lie behind them (LAMBDAS) where they fit, else they are
+//     read per row: whether factors are shared must not depend on them, because the order of a row's sums
+//     goes with it and the codes are those of the h that the unquantized call stores.
 //   - A stage holds rows of C G 8 values, zero past D, and so do the factors: the sums need no test for
 //     the row's end (a test per chunk and use was a fifth of the instructions).
 // Measured on B200, D = 3072, bf16: gate, post-norm, residual and modulated LayerNorm of two samples of 16896 rows
 // 137 us (6.1 TB/s, 0.93 of a copy), of 4608 rows 25.5 us; a modulated LayerNorm of 4608 rows 12.6 us, of one row 4.2.
 // Every wait is bounded: one that runs out sets the status word and the block's abort flag, later waits
 // then return at once, and the group's remaining copies are waited for before it leaves.
-template <int C, int R, bool XF32, int Y, bool QUANT, bool SHARE>
+template <int C, int R, bool XF32, int Y, bool QUANT, bool SHARE, bool LAMBDAS = QUANT && SHARE>
 __global__ void __launch_bounds__(32 * kMaxWarps, 1)
     block_norm_kernel(const __grid_constant__ Args a, int G, int stages, int factor_sets, unsigned long long wait_ns) {
   constexpr bool has_y = Y != kNoY;
@@ -487,10 +490,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
     q[0] = make_float4(v[0], v[1], v[2], v[3]);
     q[G] = make_float4(v[4], v[5], v[6], v[7]);
   };
-  // the smoothing reciprocals of a quantized output: SHARE laid out like a factor behind the factor sets
+  // the smoothing reciprocals of a quantized output: LAMBDAS laid out like a factor behind the factor sets
   float* const lambdas = factors + factor_sets * (has_y ? 3 : 2) * span;
   auto smooth = [&](int c) -> F8 {
-    if constexpr (SHARE) {
+    if constexpr (LAMBDAS) {
       const float4* q = reinterpret_cast<const float4*>(lambdas) + 2 * c * G + t;
       return join(q[0], q[G]);
     } else {
@@ -532,7 +535,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1)
   };
 
   for (int i = 0; i < stages; ++i) fetch(i);
-  if constexpr (QUANT && SHARE) {
+  if constexpr (LAMBDAS) {
     for (int c = group; c < C; c += groups) {
       float l[8];
       vec8<true>(l, Vec{a.inv_lambda, 0, 1}, 0, c, D, G, t);

@@ -470,3 +470,27 @@ def test_quantized_offsets_past_the_rows(cuda_device):
         ref_act = svdq.quantize_act_mx(want[1], w, svdq.MxAct(M, D, 0, "cuda"))
         for u, v in zip(svdq.export_act_mx(act), svdq.export_act_mx(ref_act)):
             assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("D,xt,yt", [(8200, BF16, BF16), (12288, BF16, BF16), (12296, BF16, None), (16384, F32, None),
+                                     (16384, BF16, None), (12288, F32, BF16)])
+def test_quantized_wide_rows_are_the_unfused_chain(cuda_device, D, xt, yt):
+    """Many rows so wide that shared factors leave no room for the smoothing reciprocals: the sums of both
+    forms run in the same order, so that codes and scales are those of the stored h."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    T = 310
+    x, w = _rand(g, T, D, dtype=xt, std=3.0), _mx_weight(g, 128, D)
+    gate, scale, shift = _rand(g, 3, D, std=0.5)
+    norm, act = _norm(g, "layer", D, True), svdq.MxAct(T, D, 0, "cuda")
+    if yt is None:
+        h = svdq.block_norm(x, norm, scale, shift, out_dtype=BF16)
+        svdq.norm_quantize_act_mx(x, norm, w, act, scale, shift)
+    else:
+        y, post = _rand(g, T, D, dtype=yt), _norm(g, "rms", D, True)
+        kw = dict(gate=gate, post=post, scale=scale, shift=shift)
+        xo, h = svdq.gated_residual(x, y, norm=norm, h_dtype=BF16, **kw)
+        got, _ = svdq.gated_residual_quantize_mx(x, y, norm, w, act, **kw)
+        assert torch.equal(got, xo)
+    want = svdq.quantize_act_mx(h, w, svdq.MxAct(T, D, 0, "cuda"))
+    for u, v in zip(svdq.export_act_mx(act), svdq.export_act_mx(want)):
+        assert torch.equal(u, v), (u != v).sum()
