@@ -2256,14 +2256,14 @@ template <bool XF32, int Y, bool QUANT>
 NormKernel norm_kernel(int chunks, bool share) {
   using namespace svdq::norm;
   if (!share)
-    return chunks <= 2 ? block_norm_kernel<2, norm_batch(2), XF32, Y, QUANT, false>
-                       : block_norm_kernel<8, norm_batch(8), XF32, Y, QUANT, false>;
+    return chunks <= 2   ? block_norm_kernel<2, norm_batch(2), XF32, Y, QUANT, false>
+           : chunks <= 6 ? block_norm_kernel<6, norm_batch(6), XF32, Y, QUANT, false>
+                         : block_norm_kernel<8, norm_batch(8), XF32, Y, QUANT, false>;
   switch (chunks) {
     case 1: return block_norm_kernel<1, norm_batch(1), XF32, Y, QUANT, true>;
     case 2: return block_norm_kernel<2, norm_batch(2), XF32, Y, QUANT, true>;
     case 4: return block_norm_kernel<4, norm_batch(4), XF32, Y, QUANT, true>;
-    case 6: return block_norm_kernel<6, norm_batch(6), XF32, Y, QUANT, true>;
-    default: return block_norm_kernel<8, norm_batch(8), XF32, Y, QUANT, true>;
+    default: return block_norm_kernel<6, norm_batch(6), XF32, Y, QUANT, true>;  // eight leave no room for factors
   }
 }
 template <bool XF32, bool QUANT>
@@ -2296,6 +2296,10 @@ cudaError_t launch_norm_any(const cudaLaunchConfig_t& cfg, int chunks, const svd
 }
 
 constexpr int kNormSmem = 212 * 1024;  // the most a block's rings take
+// fp32 x and y wider than this (six chunks for each of 512 threads) do not fit them: the element-wise kernel's
+// rows, and refused with a quantized output. All other rows up to kNormMaxD fit.
+constexpr int kNormMaxF32Pair = 6 * 512 * 8;
+static_assert(kNormMaxF32Pair * 8 <= kNormSmem && kNormMaxD * 6 <= kNormSmem, "rows that fit");
 struct NormState {
   bool ready = false;
 };
@@ -2381,8 +2385,8 @@ svdq_status run_norm(const svdq_block_norm_args* a, const svdq_mx_weight* w, con
     const auto stage_bytes = [&] { return norm_batch(chunks) * chunks * 256 * W * elem_bytes; };
     const auto factor_bytes = [&] { return chunks * 256 * W * (a->y ? 12 : 8); };
     // Factors of a run's sample in shared memory where a run gives every group two batches and the SMs have
-    // more than two rows each; else (or where they do not fit beside a batch) two or eight chunks per thread
-    // and vectors read per row, which with few rows is sooner done: 24 and 296 rows of 3072, gate, post-norm,
+    // more than two rows each; else (or where they do not fit beside a batch) two, six or eight chunks per
+    // thread and vectors read per row, which with few rows is sooner done: 24 and 296 rows of 3072, gate, post-norm,
     // residual and norm 6.4 and 6.9 us against 7.2 with shared factors, quantized 7.5 against 9.0 (24 rows),
     // a norm alone 3.7 against 4.9; at 400 rows 7.6 / 7.3 and 4.5 / 5.1, at 600 rows 10.4 / 7.4 and 5.7 / 5.2.
     const int per_run = a->offsets ? a->M / a->samples : a->rows_per_sample;
@@ -2394,9 +2398,10 @@ svdq_status run_norm(const svdq_block_norm_args* a, const svdq_mx_weight* w, con
     if (far_lambdas) lambda_bytes = 0;
     if (!share) {
       W = row_warps(2);
-      chunks = (eights + 32 * W - 1) / (32 * W) <= 2 ? 2 : 8;
+      const int need = (eights + 32 * W - 1) / (32 * W);
+      chunks = need <= 2 ? 2 : need <= 6 ? 6 : 8;
     }
-    if (stage_bytes() <= kNormSmem) {
+    if (stage_bytes() <= kNormSmem) {  // but for fp32 x and y wider than kNormMaxF32Pair
       // Rows in flight per SM: as many groups as fit a block, but no more than about 80 KB of batches; a
       // second stage where that leaves room for one. Measured on B200 over two samples of 16896 rows of
       // 3072, all bf16 (12 KB of x and y): 6 groups 137 us, 8 groups 157 us, 4 groups 171 us, 6 groups with
@@ -2433,9 +2438,6 @@ svdq_status run_norm(const svdq_block_norm_args* a, const svdq_mx_weight* w, con
         return fail(SVDQ_ERR_CUDA, "launch of norm::block_norm_kernel failed: %s", cudaGetErrorString(e));
       return check_launch("norm::block_norm_kernel");
     }
-    if (act)
-      return fail(SVDQ_ERR_UNSUPPORTED, "rows of x and y of %d bytes (at most %d with a quantized output)", stage_bytes(),
-                  kNormSmem);
   }
   W = row_warps(1);
   chunks = whole((eights + 32 * W - 1) / (32 * W));
@@ -2472,6 +2474,9 @@ svdq_status svdq_block_norm_quantize_mx(const svdq_block_norm_args* a, const svd
     return fail(SVDQ_ERR_UNSUPPORTED, "a branch of rank %d projects h: use svdq_block_norm and svdq_mx_quantize_act",
                 w->r ? w->r : act->r);
   if (!norm_vectorised(a)) return fail(SVDQ_ERR_UNSUPPORTED, "a quantized output needs 16-byte aligned rows and vectors");
+  if (a->y != nullptr && a->x_f32 && a->y_f32 && a->D > kNormMaxF32Pair)
+    return fail(SVDQ_ERR_UNSUPPORTED, "fp32 rows of x and y of %d values (at most %d with a quantized output)", a->D,
+                kNormMaxF32Pair);
   int sms;
   if (svdq_status s = norm_ready(&sms); s != SVDQ_OK) return s;
   return run_norm(a, w, act, true, sms, stream);

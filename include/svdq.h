@@ -400,7 +400,7 @@ SVDQ_API svdq_status svdq_mx_dequantize_act(const svdq_mx_act* act, void* out, l
  * at m * row stride, and rows outside every sample are neither read nor written.
  * x_out may be x itself (same strides); no other output may share memory with an input or output.
  * 1 <= D <= 32768; any strides and element alignment (16-byte aligned rows and vectors with D a
- * multiple of 8 take the fast path). */
+ * multiple of 8 take the fast path, up to D = 24576 where x and y are both fp32). */
 typedef enum { SVDQ_NORM_NONE = 0, SVDQ_NORM_RMS = 1, SVDQ_NORM_LAYER = 2 } svdq_norm_kind;
 
 typedef struct svdq_norm {   /* one normalisation: kind, eps and its vectors */
@@ -435,8 +435,8 @@ SVDQ_API svdq_status svdq_block_norm(const svdq_block_norm_args* a, svdq_stream_
 /* The same pass with bf16(h) quantized for the next layer instead of (or beside) being stored: the
  * codes and scales are those svdq_mx_quantize_act makes of h. `act` is bound with M = a->M, K = a->D;
  * w supplies inv_lambda (w->K == a->D) and has no branch (w->r == 0: a branch projects h itself, so
- * use svdq_block_norm with h and svdq_mx_quantize_act). D % 8 == 0, 16-byte aligned rows and
- * vectors. Rows outside every sample are quantized as zero. */
+ * use svdq_block_norm with h and svdq_mx_quantize_act). D % 8 == 0, D <= 24576 where x and y are both
+ * fp32, 16-byte aligned rows and vectors. Rows outside every sample are quantized as zero. */
 SVDQ_API svdq_status svdq_block_norm_quantize_mx(const svdq_block_norm_args* a, const svdq_mx_weight* w,
                                         const svdq_mx_act* act, svdq_stream_t stream);
 

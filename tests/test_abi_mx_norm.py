@@ -245,6 +245,21 @@ def test_block_norm_quantize_refusals(L):
     assert L.svdq_block_norm_quantize_mx(None, ctypes.byref(w), ctypes.byref(act), None) == 1
 
 
+def test_quantized_rows_up_to_the_stated_width(L):
+    """Every width up to 32768 in whole groups of 8 is taken, but 24576 at most where x and y are both fp32."""
+    def call(D, x_f32, y_f32, **kw):
+        act, w = _pair(L, M=12, K=D, N=1000, r=0)
+        w.K_pad = act.K_pad
+        args = _norm_args(D=D, ldx=D, ldy=D, ld_out=D, ld_gate=D, x_f32=x_f32, y_f32=y_f32, h=None, x=BASE, y=BASE + (8 << 20),
+                          x_out=BASE + (16 << 20), gate=BASE + (24 << 20), **kw)
+        return L.svdq_block_norm_quantize_mx(ctypes.byref(args), ctypes.byref(w), ctypes.byref(act), None)
+    assert call(24584, 1, 1) == 2 and b"24576" in L.svdq_last_error()
+    assert call(32768, 1, 1) == 2
+    if not torch.cuda.is_available():                               # well-formed: stops at the device
+        for D, x_f32, y_f32 in ((8200, 1, 1), (12288, 1, 1), (24576, 1, 1), (32768, 1, 0), (32768, 0, 1), (32768, 0, 0)):
+            assert call(D, x_f32, y_f32) == 3, L.svdq_last_error()
+
+
 def test_binding_refuses_before_the_library(L):
     cpu = torch.zeros(4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):

@@ -494,3 +494,21 @@ def test_quantized_wide_rows_are_the_unfused_chain(cuda_device, D, xt, yt):
     want = svdq.quantize_act_mx(h, w, svdq.MxAct(T, D, 0, "cuda"))
     for u, v in zip(svdq.export_act_mx(act), svdq.export_act_mx(want)):
         assert torch.equal(u, v), (u != v).sum()
+
+
+@pytest.mark.parametrize("T", [3, 300])
+@pytest.mark.parametrize("D,xt,yt", [(3072, F32, F32), (8192, F32, F32), (8200, F32, F32), (12288, F32, F32), (24576, F32, F32),
+                                     (8200, F32, BF16), (32768, F32, BF16), (264, BF16, F32), (32768, BF16, F32)])
+def test_quantized_fp32_rows_are_the_unfused_chain(cuda_device, D, xt, yt, T):
+    """fp32 streams and block outputs at every width that the quantized form takes."""
+    g = torch.Generator(device="cuda").manual_seed(D + T)
+    x, y, w = _rand(g, T, D, dtype=xt, std=3.0), _rand(g, T, D, dtype=yt), _mx_weight(g, 128, D)
+    gate, scale, shift = _rand(g, 3, D, std=0.5)
+    kw = dict(gate=gate, post=_norm(g, "layer", D, True), scale=scale, shift=shift, res_scale=0.5)
+    norm, act = _norm(g, "rms", D, True), svdq.MxAct(T, D, 0, "cuda")
+    xo, h = svdq.gated_residual(x, y, norm=norm, h_dtype=BF16, **kw)
+    got, _ = svdq.gated_residual_quantize_mx(x, y, norm, w, act, **kw)
+    assert torch.equal(got, xo)
+    want = svdq.quantize_act_mx(h, w, svdq.MxAct(T, D, 0, "cuda"))
+    for u, v in zip(svdq.export_act_mx(act), svdq.export_act_mx(want)):
+        assert torch.equal(u, v), (u != v).sum()
