@@ -21,6 +21,7 @@ EPI_NONE, EPI_BIAS, EPI_SWIGLU, EPI_BIAS_SWIGLU = 0, 1, 2, 3
 OUT_BF16, OUT_F32 = 0, 1
 STATUS_NAMES = {0: "SVDQ_OK", 1: "SVDQ_ERR_INVALID_ARG", 2: "SVDQ_ERR_UNSUPPORTED", 3: "SVDQ_ERR_CUDA",
                 4: "SVDQ_ERR_TIMEOUT"}
+ERR_UNSUPPORTED = 2
 
 
 class SvdqWeight(ctypes.Structure):
@@ -883,6 +884,19 @@ def gated_residual_quantize_mx(x, y, norm: Norm, w: MxWeight, act: MxAct, gate=N
     return out, act
 
 
+def _norm_into_act_mx(x, norm, w, act, scale, shift, offsets):
+    """The quantized norm of x in one pass, or by way of a stored h: for a branch, which projects h, and for rows
+    that the pass refuses (off 16 bytes, say)."""
+    if w.r == 0:
+        try:
+            return norm_quantize_act_mx(x, norm, w, act, scale, shift, offsets)
+        except SvdqError as e:
+            if e.status != ERR_UNSUPPORTED:
+                raise
+    h = block_norm(x, norm, scale, shift, offsets, out_dtype=torch.bfloat16)
+    return quantize_act_mx(h.view(-1, w.K), w, act)
+
+
 def mlp_mx(x, w_up: MxWeight, w_down: MxWeight, bias_up=None, bias_down=None, norm: Norm | None = None, scale=None,
            shift=None, post: Norm | None = None, gate=None, res_scale: float = 1.0, skip_scale: float = 1.0, offsets=None,
            acts: tuple[MxAct, MxAct] | None = None, out=None):
@@ -891,7 +905,7 @@ def mlp_mx(x, w_up: MxWeight, w_down: MxWeight, bias_up=None, bias_down=None, no
     [samples, rows, K], bf16 or fp32):
         skip_scale x + res_scale gate post(mlp(norm(x) (1 + scale) + shift))
     in x's type, with samples, `offsets` and `out` as in gated_residual. The norm's result is quantized
-    where it is computed if w_up has no branch. acts: the activation buffers of the two layers, for
+    where it is computed if w_up has no branch and x's rows and the vectors lie on 16 bytes. acts: the activation buffers of the two layers, for
     callers that keep them."""
     if not w_up.swiglu or w_down.K != w_up.N // 2:
         raise ValueError(f"w_up must be packed with swiglu=True and w_down take its {w_up.N // 2} outputs, not {w_down.K}")
@@ -906,11 +920,8 @@ def mlp_mx(x, w_up: MxWeight, w_down: MxWeight, bias_up=None, bias_down=None, no
     act_up, act_down = acts or (MxAct(rows, w_up.K, w_up.r, x.device), MxAct(rows, w_down.K, w_down.r, x.device))
     if norm is None:
         quantize_act_mx(x, w_up, act_up)
-    elif w_up.r == 0:
-        norm_quantize_act_mx(x, norm, w_up, act_up, scale, shift, offsets)
     else:
-        h = block_norm(x, norm, scale, shift, offsets, out_dtype=torch.bfloat16)
-        quantize_act_mx(h.view(rows, w_up.K), w_up, act_up)
+        _norm_into_act_mx(x, norm, w_up, act_up, scale, shift, offsets)
     y = linear_mx(gemm_mx(act_up, w_up, bias_up), w_down, bias_down, act_down, out=out if norm is None else None)
     if norm is None:
         return y

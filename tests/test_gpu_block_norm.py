@@ -512,3 +512,24 @@ def test_quantized_fp32_rows_are_the_unfused_chain(cuda_device, D, xt, yt, T):
     want = svdq.quantize_act_mx(h, w, svdq.MxAct(T, D, 0, "cuda"))
     for u, v in zip(svdq.export_act_mx(act), svdq.export_act_mx(want)):
         assert torch.equal(u, v), (u != v).sum()
+
+
+@pytest.mark.parametrize("left", ["x", "mods"])
+def test_mlp_block_of_misaligned_slices(cuda_device, left):
+    """A layer without a branch takes slices that do not start on 16 bytes, as one with a branch does."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    B, T, D, F = 2, 30, 256, 384
+    at_x, at_m = (3, 0) if left == "x" else (0, 5)
+    x = _rand(g, B, T, D + 8)[..., at_x:at_x + D]
+    scale, shift = (_rand(g, B, D + 16, std=0.5)[:, at_m:at_m + D] for _ in range(2))
+    norm = _norm(g, "layer", D, False)
+    up = svdq.MxWeight(_rand(g, 2 * F, D, dtype=F32, std=D ** -0.5), swiglu=True)
+    down = svdq.MxWeight(_rand(g, D, F, dtype=F32, std=F ** -0.5))
+    got = svdq.mlp_mx(x, up, down, norm=norm, scale=scale, shift=shift)
+    h = svdq.block_norm(x, norm, scale, shift, out_dtype=BF16)
+    y = svdq.mlp_mx(h.view(-1, D), up, down)
+    assert torch.equal(got, svdq.gated_residual(x, y.view(B, T, D)))
+    with pytest.raises(svdq.SvdqError, match="16-byte"):            # the pass itself still refuses them
+        svdq.norm_quantize_act_mx(x, norm, up, svdq.MxAct(B * T, D, 0, "cuda"), scale, shift)
+    with pytest.raises(svdq.SvdqError, match="do not match"):       # other refusals stay refusals
+        svdq.mlp_mx(x, up, down, norm=norm, acts=(svdq.MxAct(7, D, 0, "cuda"), svdq.MxAct(7, F, 0, "cuda")))
