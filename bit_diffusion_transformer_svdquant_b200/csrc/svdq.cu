@@ -1552,15 +1552,31 @@ int mx_n_pad(int N, int swiglu) {
 // K = 3072, r = 32: 3.9 (one row) to 8.6 (384) against kernel 1's 11.0, 14.9 / 11.1 at 512; K = 12288, r = 32:
 // 7.8 to 24.1 against 26.3, 41 / 27 at 512; K = 1024, r = 32: 5.6 / 7.0 at 384; K = 3072, r = 0: 1.5 to 4.3 against
 // 6.9, 7.2 / 6.6 at 2048; K = 1024, r = 0: 3.0 / 3.6 at 1024, 3.9 / 3.6 at 1536.
-// The product up to 32 rows, and up to 128 where splitting K over the SMs outweighs its epilogue of M x N sums:
-// 3072 -> 9216 7.7 against the pair GEMM's 9.3 at one row, 9.1 / 9.4 at 40, 10.0 / 9.5 at 64; 3072 -> 3072 6.9 / 8.3
-// at 64, 8.4 / 8.5 at 128; 12288 -> 3072 10.2 / 21.3 at one row, 13.3 / 21.7 at 128; 256 -> 9216 4.0 / 4.9 at 16,
-// 5.4 / 5.0 at 40; 3072 -> 24576 with SwiGLU 12.8 / 16.2 at one row, 16.3 / 16.4 at 64.
 bool mx_few_quant_rows(int M, int K_pad, int r) {
   return r == 0 ? M <= 1024 : M <= 384 && K_pad <= kFewQuantMaxK;
 }
-bool mx_few_product_rows(int M, int K_pad, int N) {
-  return M <= 32 || (M <= svdq::mx::kFewCols && 128ll * K_pad >= 1ll * M * N);
+// The product up to 32 rows, and up to 128 (SwiGLU 64) where splitting K over the SMs outweighs its epilogue of M x N
+// sums, r = 32: 3072 -> 9216 7.7 against the pair GEMM's 9.3 at one row, 9.1 / 9.4 at 40, 10.0 / 9.5 at 64; 3072 -> 3072
+// 6.9 / 8.3 at 64, 8.4 / 8.5 at 128; 12288 -> 3072 10.2 / 21.3 at one row, 13.3 / 21.7 at 128; 256 -> 9216 4.0 / 4.9 at 16,
+// 5.4 / 5.0 at 40; 3072 -> 24576 with SwiGLU 12.8 / 16.2 at one row, 16.3 / 16.4 at 64.
+// A CTA with a single K step (no branch and K split down to that) has little but the epilogue, which its cluster shares:
+// up to 8 rows per CTA of the cluster, 16 at least, and while all blocks run at once: 256 -> 9216 3.1 / 4.7 at one row,
+// 3.5 / 4.7 at 16, 256 -> 128 4.2 / 3.6 at 32, 256 -> 24576 6.9 / 6.0 at one row; 512 -> 3072 3.7 / 4.2 and 4.6 / 4.2 at
+// 32; 1024 -> 1024 3.7 / 4.7, 4.5 / 4.8 at 32, 5.2 / 4.9 at 64; 2048 -> 1024 4.0 / 6.3, 5.4 / 6.4 at 64, 6.5 / 6.5 at 128;
+// SwiGLU 256 -> 24576 4.1 / 7.2, 2048 -> 2048 4.6 / 7.3, 7.4 / 7.5 at 64.
+struct FewSplit {
+  int blocks, ranks;  // CTA clusters over N, and their size over K
+};
+FewSplit mx_few_split(const svdq_mx_weight* w, bool swiglu, int dev) {
+  FewSplit s{swiglu ? w->N_pad / 256 : (w->N + 127) / 128, 1};
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  for (int i = 1; i < 4; ++i)
+    if (s.blocks <= g_mx[dev].few_clusters[i] && (1 << i) <= w->K_pad / 256) s.ranks = 1 << i;
+  return s;
+}
+bool mx_few_product_rows(int M, const svdq_mx_weight* w, bool swiglu, const FewSplit& s, int sms) {
+  if (w->r == 0 && w->K_pad / 256 == s.ranks) return M <= (s.ranks > 2 ? 8 * s.ranks : 16) && s.blocks <= sms;
+  return M <= 32 || (M <= svdq::mx::few_max_cols(swiglu ? 2 : 1) && 128ll * w->K_pad >= 1ll * M * w->N);
 }
 
 struct MxWeightLayout {
@@ -1625,28 +1641,27 @@ svdq_status check_mx_act(const svdq_mx_act* a) {
   return SVDQ_OK;
 }
 
-// The few-row product; *done stays false where the pair GEMM is to run (no split of K that fits).
+// The few-row product of what mx_few_product_rows takes.
 svdq_status mx_few_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const uint16_t* bias, bool has_bias, bool swiglu,
-                        void* Y, long long ldy, int esize, int dev, svdq_stream_t stream, bool* done) {
+                        void* Y, long long ldy, int esize, const FewSplit& split, svdq_stream_t stream) {
+  using namespace svdq::mx;
+  static_assert(2 * few_stage_bytes(1, few_max_cols(1)) + few_part_bytes(1, few_max_cols(1)) + 1024 <= kFewMaxSmem &&
+                    2 * few_stage_bytes(2, few_max_cols(2)) + few_part_bytes(2, few_max_cols(2)) + 1024 <= kFewMaxSmem,
+                "two stages always fit");
+  static_assert(few_max_cols(1) + kFewMaxStages * few_stage_tmem(1) <= 512 &&
+                    2 * few_max_cols(2) + kFewMaxStages * few_stage_tmem(2) <= 512,
+                "TMEM budget");
   const int NB = swiglu ? 2 : 1, r = w->r;
   const int cols = act->M <= 16 ? 16 : act->M <= 32 ? 32 : act->M <= 64 ? 64 : 128;
-  const int blocks = swiglu ? w->N_pad / 256 : (w->N + 127) / 128, steps = w->K_pad / 256;
-  int ranks_log = 0;
-  {
-    std::lock_guard<std::mutex> lk(g_dev_mu);
-    for (int i = 1; i < 4; ++i)
-      if (blocks <= g_mx[dev].few_clusters[i] && (1 << i) <= steps) ranks_log = i;
-  }
-  const int ranks = 1 << ranks_log;
-  const int stage = svdq::mx::few_stage_bytes(NB, cols);
-  const int part = svdq::mx::few_part_bytes(NB, cols);
+  const int blocks = split.blocks, ranks = split.ranks, steps = w->K_pad / 256;
+  const int stage = few_stage_bytes(NB, cols);
+  const int part = few_part_bytes(NB, cols);
   const int slots = (steps + ranks - 1) / ranks + (r + 31) / 32;
   int stages = (kFewMaxSmem - 1024 - part) / stage;
-  if (stages > slots) stages = slots;
-  if (stages > 12) stages = 12;
+  if (stages > slots) stages = slots;  // one, where a CTA has a single K step and no branch
+  if (stages > kFewMaxStages) stages = kFewMaxStages;
   int tmem = 32;
-  while (tmem < NB * cols + stages * svdq::mx::few_stage_tmem(NB)) tmem *= 2;
-  if (stages < 2 || tmem > 512) return SVDQ_OK;
+  while (tmem < NB * cols + stages * few_stage_tmem(NB)) tmem *= 2;
   CUtensorMap tmW, tmX, tmU, tmL2;
   std::memset(&tmU, 0, sizeof(tmU));
   std::memcpy(&tmW, &w->tmap[3][0], sizeof(CUtensorMap));
@@ -1696,7 +1711,6 @@ svdq_status mx_few_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const u
   const cudaError_t e = cudaLaunchKernelEx(&cfg, NB == 2 ? svdq::mx::few_gemm_kernel<2> : svdq::mx::few_gemm_kernel<1>,
                                            tmW, tmX, tmU, tmL2, g);
   if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, "launch of mx::few_gemm_kernel failed: %s", cudaGetErrorString(e));
-  *done = true;
   return check_launch("mx::few_gemm_kernel");
 }
 
@@ -1980,12 +1994,8 @@ svdq_status mx_gemm(const svdq_mx_act* act, const svdq_mx_weight* w, const uint1
   int dev, sms;
   if (svdq_status s = mx_ready(&dev, &sms); s != SVDQ_OK) return s;
 
-  if (mx_few_product_rows(act->M, act->K_pad, w->N)) {
-    bool done = false;
-    if (svdq_status s = mx_few_gemm(act, w, bias, has_bias, swiglu, Y, ldy, esize, dev, stream, &done);
-        s != SVDQ_OK || done)
-      return s;
-  }
+  if (const FewSplit split = mx_few_split(w, swiglu, dev); mx_few_product_rows(act->M, w, swiglu, split, sms))
+    return mx_few_gemm(act, w, bias, has_bias, swiglu, Y, ldy, esize, split, stream);
   const int r = w->r, n_tile = w->n_tile;
   CUtensorMap tmA, tmU, tmB, tmL2, tmY;
   std::memset(&tmU, 0, sizeof(tmU));

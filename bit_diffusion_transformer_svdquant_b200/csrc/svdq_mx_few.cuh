@@ -26,7 +26,10 @@
 namespace svdq {
 namespace mx {
 
-constexpr int kFewCols = 128;  // the product's tokens at most
+// The product's tokens at most, for NB blocks of weight rows per CTA: two (SwiGLU) leave room for two ring
+// stages beside the sums of 64 tokens only.
+__host__ __device__ constexpr int few_max_cols(int NB) { return NB == 2 ? 64 : 128; }
+constexpr int kFewMaxStages = 12;
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     few_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                     const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmL2,
                     const FewGemmArgs a) {
-  constexpr int kMaxStages = 12;
+  constexpr int kMaxStages = kFewMaxStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2];

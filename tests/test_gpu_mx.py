@@ -247,3 +247,40 @@ def test_128_wide_tiles_of_a_wider_packing(cuda_device, M, K, N, r):
     """Few enough blocks for 128-wide tiles, on weights packed 384 and 256 wide whose last tile is partly
     padding."""
     _check(*_layer(M, K, N, r, M + 5 * N, True), False, cuda_device)
+
+
+def _product_kernel(act, w):
+    """The name of the kernel that gemm_mx launches."""
+    svdq.gemm_mx(act, w)
+    torch.cuda.synchronize()
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CUDA], acc_events=True) as p:
+        svdq.gemm_mx(act, w)
+        torch.cuda.synchronize()
+    return [n for n in ("few_gemm_kernel", "pair_gemm_kernel") if any(n in e.key for e in p.key_averages())]
+
+
+@pytest.mark.parametrize("K,N,swiglu,few", [
+    # K split down to one step per CTA, no branch: few rows as far as the cluster shares the epilogue
+    (256, 1024, False, 16), (512, 640, False, 16), (1024, 768, False, 32), (2048, 512, False, 64), (1800, 256, False, 64),
+    (256, 2048, True, 16), (1024, 512, True, 32), (2048, 768, True, 64),
+    # more than one step
+    (1536, 256, False, 128), (2304, 256, False, 128), (1280, 512, True, 64)])
+def test_single_step_products(cuda_device, K, N, swiglu, few):
+    """Layers without a branch on both sides of the few-row product's rule, and which kernel took them."""
+    X, prep, bias = _layer(few + 1, K, N, 0, K + N, True)
+    w, Xd = _weight(prep, cuda_device, swiglu), to_dev_bf16(X, cuda_device)
+    for M in sorted({1, 15, few, few + 1}):
+        _check(X[:M], prep, bias, swiglu, cuda_device)
+        act = svdq.quantize_act_mx(Xd[:M], w, svdq.MxAct(M, K, 0, cuda_device))
+        assert _product_kernel(act, w) == ["few_gemm_kernel" if M <= few else "pair_gemm_kernel"], M
+
+
+@pytest.mark.parametrize("M", [64, 65, 128])
+@pytest.mark.parametrize("r", [0, 32])
+def test_few_swiglu_rows_end_at_64(cuda_device, M, r):
+    """Two accumulators of weight rows leave room for 64 tokens."""
+    X, prep, bias = _layer(M, 3072, 512, r, M + r, True)
+    _check(X, prep, bias, True, cuda_device)
+    w = _weight(prep, cuda_device, True)
+    act = svdq.quantize_act_mx(to_dev_bf16(X, cuda_device), w, svdq.MxAct(M, 3072, r, cuda_device))
+    assert _product_kernel(act, w) == ["few_gemm_kernel" if M <= 64 else "pair_gemm_kernel"]
