@@ -519,8 +519,7 @@ def _rows(t, dtype, name, rows, dim, device=None):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected ({rows}, {dim})")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    ld = t.stride(0)
-    return ld if rows > 1 or ld > dim else dim
+    return t.stride(0) if rows > 1 else dim  # a single row's stride says nothing
 
 
 def _same_device(device, **tensors):

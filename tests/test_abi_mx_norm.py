@@ -332,6 +332,13 @@ def test_no_rows_to_quantize_are_refused():
         svdq.gated_residual_quantize_mx(x, x, svdq.Norm("rms"), None, Act, out=x)
 
 
+@pytest.mark.parametrize("rows,stride,ld", [(1, 67, 64), (1, 0, 64), (1, 64, 64), (3, 72, 72), (3, 67, 67)])
+def test_the_stride_of_a_single_row_is_not_used(rows, stride, ld):
+    """One row of a wider or odder matrix is taken like a row of its own."""
+    t = torch.zeros(1024, dtype=torch.bfloat16).as_strided((rows, 64), (stride, 1))
+    assert svdq._lib._rows(_AsIfOnDevice(t), torch.bfloat16, "X", rows, 64) == ld
+
+
 def test_a_norm_follows_its_vectors():
     def vector(*shape, dtype=torch.float32):
         return _AsIfOnDevice(torch.ones(*shape, dtype=dtype))
