@@ -533,3 +533,41 @@ def test_mlp_block_of_misaligned_slices(cuda_device, left):
         svdq.norm_quantize_act_mx(x, norm, up, svdq.MxAct(B * T, D, 0, "cuda"), scale, shift)
     with pytest.raises(svdq.SvdqError, match="do not match"):       # other refusals stay refusals
         svdq.mlp_mx(x, up, down, norm=norm, acts=(svdq.MxAct(7, D, 0, "cuda"), svdq.MxAct(7, F, 0, "cuda")))
+
+
+@pytest.mark.parametrize("B,T,D", [(2, 5, 96), (1, 9, 1001), (2, 160, 3072), (1, 310, 1544), (1, 4, 12288)])
+def test_fp32_block_output_on_a_bf16_stream(cuda_device, B, T, D):
+    g = torch.Generator(device="cuda").manual_seed(D + 1)
+    at = np.repeat(np.arange(B), T)
+    x, y = _rand(g, B, T, D, std=4.0), _rand(g, B, T, D, dtype=F32, std=2.0, mean=0.5)
+    gate, scale, shift = _rand(g, B, 3 * D, std=0.5).split(D, dim=1)
+    post, norm = _norm(g, "layer", D, True), _norm(g, "rms", D, False)
+    xo, e, h, he = _run(x, y, at, gate, post, 1.0, 0.5, norm, scale, shift)
+    got_x, got_h = svdq.gated_residual(x, y, gate=gate, post=post, res_scale=0.5, norm=norm, scale=scale, shift=shift)
+    assert got_x.dtype == BF16 and got_h.dtype == F32
+    _check(got_x.reshape(-1, D), xo, e, BF16, "x'")
+    _check(got_h.reshape(-1, D), h, he, F32, "h")
+
+
+@pytest.mark.parametrize("T", [20, 330])
+@pytest.mark.parametrize("D,ht", [(264, BF16), (3072, F32), (8200, BF16)])
+def test_h_stored_beside_its_codes(cuda_device, D, ht, T):
+    """The C call's form with both outputs: h as the unquantized call stores it, and its codes."""
+    g = torch.Generator(device="cuda").manual_seed(D + T)
+    x, y, w = _rand(g, T, D, std=3.0), _rand(g, T, D), _mx_weight(g, 128, D)
+    scale, shift = _rand(g, 2, D, std=0.5)
+    norm = _norm(g, "layer", D, True)
+    for out in (None, torch.empty_like(x)):
+        h, act = torch.full((T, D + 8), 7.0, dtype=ht, device="cuda"), svdq.MxAct(T, D, 0, "cuda")
+        args = svdq._lib._norm_args(x, None if out is None else y, None, None, 1.0, 1.0, norm, scale, shift, None, out,
+                                    h[:, :D])
+        svdq._lib._run_norm_quantize(args, x, w, act)
+        if out is None:
+            want = svdq.block_norm(x, norm, scale, shift, out_dtype=ht)
+        else:
+            xo, want = svdq.gated_residual(x, y, norm=norm, scale=scale, shift=shift, h_dtype=ht)
+            assert torch.equal(out, xo)
+        assert torch.equal(h[:, :D], want) and (h[:, D:] == 7.0).all()
+        codes = svdq.quantize_act_mx(want.to(BF16), w, svdq.MxAct(T, D, 0, "cuda"))
+        for u, v in zip(svdq.export_act_mx(act), svdq.export_act_mx(codes)):
+            assert torch.equal(u, v)
