@@ -1538,7 +1538,9 @@ int round_up(int x, int to) { return (x + to - 1) / to * to; }
 
 // Tile width a weight is packed for: 384, which streams the fewest operand bytes per flop, unless padding N
 // to it costs more than that gains over 256 (large M on B200, GEMM us at 256 / 384: 16896x3072x9216 211 / 197,
-// 4608x12288x3072 62.5 / 57.0; 1024x3072x3072, whose tiles do not fill the SMs, 10.4 / 12.0). SwiGLU pairs gate and up columns inside a tile of 256.
+// 4608x12288x3072 62.5 / 57.0). The packing serves every M, so the wide tile loses where its tiles do not fill the SMs
+// and 128-wide ones, which the same packing allows, do not all run at once (1024x3072x3072 10.4 / 12.0). SwiGLU pairs
+// gate and up columns inside a tile of 256.
 int mx_n_tile(int N, int swiglu) {
   if (swiglu) return 256;
   return round_up(N, 384) * 100ll <= round_up(N, 256) * 103ll ? 384 : 256;

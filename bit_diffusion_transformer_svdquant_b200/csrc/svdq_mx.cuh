@@ -111,7 +111,7 @@ struct ActArgs {
 // block each; the lane beside it (lane ^ 1) holds the other half, and the four lanes of a row the
 // stage's two blocks, whose scales lane b = 0 stores together. Reading X bounds the kernel, as for
 // NVFP4 (the same ring, TMA stages and branch MMAs); the scale costs one shift per block there.
-// Measured on B200: 4608 rows of 12288, r = 0, 26.7 us (5.5 TB/s of X, codes and scales), 16896 rows of 3072, r = 32,
+// Measured on B200: 4608 rows of 12288, r = 0, 26.7 us (5.4 TB/s of X, codes and scales), 16896 rows of 3072, r = 32,
 // 27 us (5.0 TB/s).
 struct Act {
   using Args = ActArgs;
@@ -359,7 +359,7 @@ __device__ __forceinline__ float2 e2m1x2_value(uint32_t byte) {
 }
 
 // The values of a quantized activation: dec(q) 2^e, exact in fp32. A thread takes 8 columns of kDeqRows
-// rows, whose loads go out together; writing the values bounds it (4608 rows of 12288 to bf16 in 25.2 us, 5.8 TB/s;
+// rows, whose loads go out together; writing the values bounds it (4608 rows of 12288 to bf16 in 25.2 us, 5.7 TB/s;
 // one row per thread 33 us).
 constexpr int kDeqRows = 4;
 template <bool F32>

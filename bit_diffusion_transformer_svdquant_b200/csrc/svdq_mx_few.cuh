@@ -2,7 +2,7 @@
 //
 // At few rows the layer streams its weight: 17/32 bytes per weight element, read once. The pair GEMM's 256-row
 // tiles then leave most of the tensor pipe and, at 24 to 72 tiles, most SMs idle, so here the roles are
-// exchanged: 128 weight rows are the MMA's M side, the tokens its N side (16 to 128 columns), and K is
+// exchanged: 128 weight rows are the MMA's M side, the tokens its N side (16 to 128 columns, SwiGLU to 64), and K is
 // split over a thread-block cluster, so that about every SM streams a share of the weight. Each CTA sums
 // its K share in TMEM; the partial sums meet in distributed shared memory, every CTA of the cluster
 // finishing its part of the tokens, in rank order (the result does not depend on timing).

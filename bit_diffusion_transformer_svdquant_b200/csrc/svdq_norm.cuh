@@ -2,11 +2,12 @@
 // its output, the gate and the residual -- in one pass over each row, optionally with the result
 // quantized to MXFP4 for the next layer (declared in svdq.h as svdq_block_norm*).
 //   x' = skip x + res gate_s . P(y),   h = Norm(x') . (1 + scale_s) + shift_s
-// A row's x, y and x' stay in registers, so x and y cross HBM once and nothing else is read but the
-// per-sample and per-channel vectors, which the rows of a sample share in L1. The mean and the centred
-// second moment are summed in fp32 in two register passes: no cancellation, whatever the mean.
-// DRAM traffic bounds it; a group of G threads shares a row, so that a row's values and its vectors fit
-// in registers and several rows are in flight per SM.
+// Rows of x and y arrive in a shared-memory ring as bulk copies and cross HBM once; y is read from the ring
+// for each of its sums and for x', which then stays in registers. The per-sample and per-channel vectors
+// are multiplied into factors that lie in shared memory for all rows of a sample (for few rows and very
+// wide ones they are read from global memory per row). The mean and the centred second moment are summed
+// in fp32 one after the other: no cancellation, whatever the mean.
+// DRAM traffic bounds it; a group of G threads shares a row, so that several rows are in flight per SM.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -281,7 +282,12 @@ constexpr int kMaxWarps = 16;     // per block, and per row
 constexpr int kMaxStages = 2;     // batches a group holds or has in flight
 
 // Rows of any alignment, one at a time straight from global memory, element by element: the path of
-// misaligned or odd-sized rows. Moments as in block_norm_kernel.
+// misaligned or odd-sized rows, and of fp32 x and y too wide for the ring. Moments as in block_norm_kernel.
+// Nothing is in flight from the next row and every vector is read again for each, so that the latency of
+// these loads bounds it, far from DRAM: on B200 a modulated LayerNorm of 4608 rows of 3071, bf16, takes 168 us
+// (the same at 3072 on the 16-byte path 13.2), with y, gate and post-norm 333 us (24.1), one row 6.3 us. Above 4096
+// values a row (two chunks and more) its values spill to local memory, 312 bytes a thread at two chunks and
+// 2.5 to 8.7 KB from four on.
 template <int C>
 __global__ void __launch_bounds__(32 * kMaxWarps) block_norm_any_kernel(const __grid_constant__ Args a, int G) {
   __shared__ float red_smem[2 * 16 * kMaxWarps];
@@ -400,7 +406,10 @@ __device__ __forceinline__ Run run_at(const Args& a, int m, int limit) {
 //   - A stage holds rows of C G 8 values, zero past D, and so do the factors: the sums need no test for
 //     the row's end (a test per chunk and use was a fifth of the instructions).
 // Measured on B200, D = 3072, bf16: gate, post-norm, residual and modulated LayerNorm of two samples of 16896 rows
-// 137 us (6.1 TB/s, 0.93 of a copy), of 4608 rows 25.5 us; a modulated LayerNorm of 4608 rows 12.6 us, of one row 4.2.
+// 137 us (6.1 TB/s, 0.93 of a copy), of 4608 rows 24.1 us; a modulated LayerNorm of 4608 rows 13.2 us, of one row 4.2.
+// Quantized, 4608 rows with y 26.8 us: no unit is full (issue 59 %, DRAM 42 % at 16896 rows); about four warps a
+// scheduler wait for shared memory and shuffles and for the instruction before. Rows of 12288 with y, 4608 of them:
+// 111 us, quantized 166 us; fp32 x and y, whose vectors are read per row there, 310 and 344 us.
 // Every wait is bounded: one that runs out sets the status word and the block's abort flag, later waits
 // then return at once, and the group's remaining copies are waited for before it leaves.
 template <int C, int R, bool XF32, int Y, bool QUANT, bool SHARE, bool LAMBDAS = QUANT && SHARE>
