@@ -805,7 +805,10 @@ def _norm_args(x, y, gate, post, res_scale, skip_scale, norm, scale, shift, offs
     post_fields = _NO_NORM if post is None else post.fields("post", D, device)
     norm_fields = _NO_NORM if norm is None else norm.fields("norm", D, device)
     py, ldy, y_f32, sy, po, ldo, so = 0, 0, 0, 0, 0, 0, 0
-    if y is not None:
+    if y is None:
+        if out is not None:
+            raise ValueError("y: expected a tensor of x's shape, got None")
+    else:
         py, ldy, y_f32, sy = _norm_rows(y, "y", shape, device)
         po, ldo, o_f32, so = _norm_rows(out, "out", shape, device)
         if o_f32 != x_f32:
@@ -858,7 +861,7 @@ def gated_residual(x, y, gate=None, post: Norm | None = None, res_scale: float =
     if norm is None and (h is not None or h_dtype is not None):
         raise ValueError("h without a norm")
     if norm is not None and h is None:
-        h = _like(x, h_dtype or y.dtype)
+        h = _like(x, h_dtype or (y if y is not None else x).dtype)
     elif h is not None and h_dtype is not None and h.dtype != h_dtype:
         raise ValueError(f"h: {h.dtype}, expected {h_dtype}")
     _run_norm(_norm_args(x, y, gate, post, res_scale, skip_scale, norm, scale, shift, offsets, out, h), x.device)

@@ -339,6 +339,18 @@ def test_the_stride_of_a_single_row_is_not_used(rows, stride, ld):
     assert svdq._lib._rows(_AsIfOnDevice(t), torch.bfloat16, "X", rows, 64) == ld
 
 
+def test_a_residual_without_a_block_output_is_refused():
+    """x' would be returned as it was allocated."""
+    class Act:
+        M = 4
+    x, norm = _AsIfOnDevice(torch.ones(4, 64)), svdq.Norm("rms")
+    for call in (lambda: svdq.gated_residual(x, None, out=x), lambda: svdq.gated_residual(x, None, norm=norm, out=x, h=x),
+                 lambda: svdq.gated_residual(x, None, norm=norm, out=x, h=x, h_dtype=torch.float32),
+                 lambda: svdq.gated_residual_quantize_mx(x, None, norm, None, Act, out=x)):
+        with pytest.raises(ValueError, match="^y: "):
+            call()
+
+
 def test_a_norm_follows_its_vectors():
     def vector(*shape, dtype=torch.float32):
         return _AsIfOnDevice(torch.ones(*shape, dtype=dtype))
