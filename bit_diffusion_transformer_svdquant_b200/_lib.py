@@ -540,6 +540,8 @@ class MxWeight:
             _need(inv_lambda, torch.float32, "inv_lambda", 1)
             if inv_lambda.shape[0] != K:
                 raise ValueError("inv_lambda must be [K]")
+        if (L1s is None) != (L2 is None):
+            raise ValueError("L1s and L2: a branch has both")
         r = 0 if L1s is None else L1s.shape[1]
         if r:
             _need(L1s, torch.bfloat16, "L1s", 2)

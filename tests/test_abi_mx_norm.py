@@ -351,6 +351,13 @@ def test_a_residual_without_a_block_output_is_refused():
             call()
 
 
+def test_half_a_branch_is_refused():
+    R, L1s, L2 = _AsIfOnDevice(torch.ones(16, 64)), torch.ones(64, 16), torch.ones(16, 16)
+    for pair in ((L1s, None), (None, L2)):
+        with pytest.raises(ValueError, match="a branch has both"):
+            svdq.MxWeight(R, *pair)
+
+
 def test_a_norm_follows_its_vectors():
     def vector(*shape, dtype=torch.float32):
         return _AsIfOnDevice(torch.ones(*shape, dtype=dtype))
