@@ -19,16 +19,96 @@ constexpr long long kMaxStride = 1ll << 38;
 
 bool at16(const void* p) { return aligned16(p); }
 
-// Bytes [lo, hi) that a [samples][rows][heads][D] tensor spans (strides are non-negative).
-struct Span {
-  uintptr_t lo, hi;
+// The bytes of a strided tensor: runs of `width` bytes at base + sum of i_d stride_d, 0 <= i_d < n_d (strides in bytes,
+// not negative).
+struct Grid {
+  uintptr_t base;
+  long long width;
+  struct {
+    long long stride, n;
+  } dim[3];
+  Grid(const void* p, long long esize, long long run, long long s0 = 0, long long n0 = 1, long long s1 = 0, long long n1 = 1,
+       long long s2 = 0, long long n2 = 1)
+      : base(reinterpret_cast<uintptr_t>(p)), width(run * esize), dim{{s0 * esize, n0}, {s1 * esize, n1}, {s2 * esize, n2}} {}
 };
-Span span(const void* p, long long sb, long long st, long long sh, int samples, int T, int heads, int D, int esize) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  const long long last = (samples - 1) * sb + (T - 1) * st + (heads - 1) * sh + D;
-  return {lo, lo + static_cast<uintptr_t>(last) * esize};
-}
-bool meet(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+// Whether two grids share a byte: whether integers k_u, one for each different stride u, make base' - base + sum of k_u u lie
+// within the runs' widths; k_u is the difference of the grids' indices along the dimensions of that stride. Strides are
+// taken from the largest down, and of each only the k_u that what lies below can still make up for: one to three
+// where strides nest, as a tensor's do. A search past kMost steps counts as shared.
+class Overlap {
+ public:
+  bool shared(const Grid& a, const Grid& b) {
+    if (reach(a) <= b.base || reach(b) <= a.base) return false;
+    add(a, -1);
+    add(b, 1);
+    before_ = a.width, after_ = b.width;
+    return search(static_cast<wide>(b.base) - static_cast<wide>(a.base), 0, false);
+  }
+  // whether two places of one grid do
+  bool itself(const Grid& g) {
+    for (const auto& d : g.dim)
+      if (d.n > 1 && d.stride < g.width) return true;
+    for (int i = 0; i < 3; ++i)
+      for (int j = 0; j < i; ++j)
+        if (g.dim[i].n > 1 && g.dim[j].n > 1 && g.dim[i].stride == g.dim[j].stride) return true;
+    add(g, -1);
+    add(g, 1);
+    before_ = after_ = g.width;
+    different_ = true;
+    return search(0, 0, false);
+  }
+
+ private:
+  using wide = __int128;  // strides below 2^40 bytes times indices below 2^31
+  static constexpr int kMost = 1 << 16;
+  struct Term {
+    long long stride, lo, hi;  // lo <= k <= hi
+    wide low, high;            // of the sum of this term and those below it
+  } term_[6];
+  int terms_ = 0, steps_ = 0;
+  long long before_, after_;
+  bool different_ = false;  // at least one k is not 0
+
+  static wide reach(const Grid& g) {
+    wide end = static_cast<wide>(g.base) + g.width;
+    for (const auto& d : g.dim) end += static_cast<wide>(d.n - 1) * d.stride;
+    return end;
+  }
+  void add(const Grid& g, int sign) {
+    for (const auto& d : g.dim) {
+      if (d.n <= 1 || d.stride == 0) continue;
+      int i = 0;
+      while (i < terms_ && term_[i].stride > d.stride) ++i;
+      if (i == terms_ || term_[i].stride != d.stride) {
+        std::copy_backward(term_ + i, term_ + terms_, term_ + terms_ + 1);
+        term_[i] = {d.stride, 0, 0, 0, 0};
+        ++terms_;
+      }
+      (sign > 0 ? term_[i].hi : term_[i].lo) += sign * (d.n - 1);
+    }
+    for (int i = terms_ - 1; i >= 0; --i) {
+      const wide below_low = i + 1 < terms_ ? term_[i + 1].low : 0, below_high = i + 1 < terms_ ? term_[i + 1].high : 0;
+      term_[i].low = below_low + static_cast<wide>(term_[i].lo) * term_[i].stride;
+      term_[i].high = below_high + static_cast<wide>(term_[i].hi) * term_[i].stride;
+    }
+  }
+  static wide floor_div(wide x, wide d) { return x / d - (x % d < 0 ? 1 : 0); }
+  // `at`: base' - base and the terms above `level`
+  bool search(wide at, int level, bool moved) {
+    if (level == terms_) return at > -after_ && at < before_ && (moved || !different_);
+    const Term& t = term_[level];
+    const wide low = level + 1 < terms_ ? term_[level + 1].low : 0, high = level + 1 < terms_ ? term_[level + 1].high : 0;
+    const wide first = std::max<wide>(t.lo, floor_div(-after_ - at - high, t.stride) + 1);
+    const wide last = std::min<wide>(t.hi, floor_div(before_ - 1 - at - low, t.stride));
+    for (wide k = first; k <= last; ++k) {
+      if (++steps_ > kMost) return true;
+      if (search(at + k * t.stride, level + 1, moved || k != 0)) return true;
+    }
+    return false;
+  }
+};
+bool meet(const Grid& a, const Grid& b) { return Overlap().shared(a, b); }
 
 svdq_status check_norm(const svdq_norm& n, const char* what, int D) {
   if (n.kind < SVDQ_NORM_NONE || n.kind > SVDQ_NORM_LAYER || (n.f32 != 0 && n.f32 != 1) ||
@@ -89,52 +169,32 @@ svdq_status check_sizes(const svdq_heads_args& a) {
   return SVDQ_OK;
 }
 
-// An output may be its own input (the same view, of one type) or apart from every input and other output; or all lie
-// in rows of one stride, in different columns of it.
+Grid input_of(const svdq_heads& h, const svdq_heads_args& a) {
+  return Grid(h.x, a.x_f32 ? 4 : 2, a.D, h.sb, a.samples, h.st, a.rows_per_sample, h.sh, h.heads);
+}
+Grid output_of(const svdq_heads& h, const svdq_heads_args& a) {
+  return Grid(h.out, a.out_f32 ? 4 : 2, a.D, h.ob, a.samples, h.ot, a.rows_per_sample, h.oh, h.heads);
+}
+bool same_view(const Grid& a, const Grid& b) {
+  if (a.base != b.base || a.width != b.width) return false;
+  for (int i = 0; i < 3; ++i)
+    if (a.dim[i].n != b.dim[i].n || (a.dim[i].n > 1 && a.dim[i].stride != b.dim[i].stride)) return false;
+  return true;
+}
+
+// An output may be its own input (the same view, of one type); else it shares no byte with an input or another output.
 svdq_status check_overlap(const svdq_heads_args& a, const svdq_heads* const* in, int n_in, const svdq_heads* const* out,
                           int n_out) {
-  const int xe = a.x_f32 ? 4 : 2, oe = a.out_f32 ? 4 : 2, T = a.rows_per_sample, B = a.samples;
-  auto beside = [&](const void* p, long long sb, long long st, long long sh, int hp, int ep, const void* q, long long qb,
-                    long long qt, long long qh, int hq, int eq) {
-    if (ep != eq || (T > 1 && st != qt) || (B > 1 && sb != qb)) return false;
-    const long long row = T > 1 ? st : sb;  // the stride that columns repeat at
-    if (T == 1 && B == 1) return false;     // one row: spans say all
-    if (T > 1 && B > 1 && sb % st != 0) return false;
-    const long long wp = (hp - 1) * sh + a.D, wq = (hq - 1) * qh + a.D;
-    if (row <= 0 || wp > row || wq > row) return false;
-    const long long d = (reinterpret_cast<intptr_t>(q) - reinterpret_cast<intptr_t>(p)) / ep;
-    const long long m = ((d % row) + row) % row;  // columns of q after those of p, around the row
-    return m >= wp && m + wq <= row;
-  };
   for (int o = 0; o < n_out; ++o) {
-    const svdq_heads& y = *out[o];
-    const Span so = span(y.out, y.ob, y.ot, y.oh, B, T, y.heads, a.D, oe);
-    // an output's own heads are apart: each of its dimensions, by stride, steps over all that the ones below it span
-    struct {
-      long long stride, n;
-    } dims[3] = {{y.ob, B}, {y.ot, T}, {y.oh, y.heads}};
-    std::sort(dims, dims + 3, [](const auto& l, const auto& r) { return l.stride < r.stride; });
-    long long extent = a.D;
-    for (const auto& d : dims) {
-      if (d.n == 1) continue;
-      if (d.stride < extent) return fail(SVDQ_ERR_INVALID_ARG, "an output's heads overlap");
-      extent += (d.n - 1) * d.stride;
-    }
+    const Grid y = output_of(*out[o], a);
+    if (Overlap().itself(y)) return fail(SVDQ_ERR_INVALID_ARG, "an output's heads overlap");
     for (int i = 0; i < n_in; ++i) {
-      const svdq_heads& x = *in[i];
-      const Span si = span(x.x, x.sb, x.st, x.sh, B, T, x.heads, a.D, xe);
-      if (!meet(so, si)) continue;
-      const bool same = &x == &y && x.x == y.out && xe == oe && (B == 1 || x.sb == y.ob) && (T == 1 || x.st == y.ot) &&
-                        (x.heads == 1 || x.sh == y.oh);
-      if (!same && !beside(y.out, y.ob, y.ot, y.oh, y.heads, oe, x.x, x.sb, x.st, x.sh, x.heads, xe))
+      const Grid x = input_of(*in[i], a);
+      if (!(in[i] == out[o] && same_view(x, y)) && meet(y, x))
         return fail(SVDQ_ERR_INVALID_ARG, "an output overlaps an input");
     }
-    for (int p = 0; p < o; ++p) {
-      const svdq_heads& z = *out[p];
-      if (meet(so, span(z.out, z.ob, z.ot, z.oh, B, T, z.heads, a.D, oe)) &&
-          !beside(y.out, y.ob, y.ot, y.oh, y.heads, oe, z.out, z.ob, z.ot, z.oh, z.heads, oe))
-        return fail(SVDQ_ERR_INVALID_ARG, "outputs overlap");
-    }
+    for (int p = 0; p < o; ++p)
+      if (meet(y, output_of(*out[p], a))) return fail(SVDQ_ERR_INVALID_ARG, "outputs overlap");
   }
   return SVDQ_OK;
 }

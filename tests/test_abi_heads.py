@@ -247,3 +247,79 @@ def test_cpu_tensors_are_refused(L):
         svdq.KvCache(4, 16, 2, 60)
     with pytest.raises(ValueError, match="CUDA"):
         svdq.KvCache(4, 16, 2, 64, device="cpu")
+
+
+# ---------------------------------------------------------------- which outputs share memory
+
+def _bytes(at, dims, width):
+    """The bytes of runs of `width` at `at` plus every sum of index x stride."""
+    starts = np.array([at], dtype=np.int64)
+    for stride, n in dims:
+        starts = (starts[:, None] + stride * np.arange(n)).ravel()
+    return starts, np.sort((starts[:, None] + np.arange(width)).ravel())
+
+
+def test_slices_in_attention_layout_share_nothing(L):
+    """q and k as slices of one [samples, 2, heads, rows, D] buffer, from inputs elsewhere and from slices of another."""
+    if torch.cuda.is_available():
+        pytest.skip("fake addresses: CPU only")
+    B, T, H, D = 2, 5, 6, 40
+    view = dict(ob=2 * H * T * D, ot=D, oh=T * D)
+    both = {f"q__{k}": v for k, v in view.items()} | {f"k__{k}": v for k, v in view.items()}
+    apart = dict(samples=B, q__sb=T * H * D, k__sb=T * H * D, k__st=H * D, k__heads=H, k__out=BASE + (1 << 24) + H * T * D * 2)
+    assert L.svdq_rotary(ctypes.byref(_args(**both, **apart)), None) == 3, L.svdq_last_error()
+    apart["k__out"] -= 2                                    # the first value of k is the last of q
+    assert L.svdq_rotary(ctypes.byref(_args(**both, **apart)), None) == 1
+    # rotated where they lie: the same slices are the inputs
+    inputs = {f"{t}__{i}": v for t in "qk" for i, v in (("sb", view["ob"]), ("st", D), ("sh", T * D))}
+    apart |= inputs | dict(k__out=BASE + (1 << 24) + H * T * D * 2, q__x=BASE + (1 << 24),
+                           k__x=BASE + (1 << 24) + H * T * D * 2)
+    assert L.svdq_rotary(ctypes.byref(_args(**both, **apart)), None) == 3, L.svdq_last_error()
+
+
+def test_overlaps_are_those_of_the_bytes(L):
+    """Small tensors of any strides and distances: refused exactly where two places of an output, or an output and another
+    tensor, share a byte (an output that is its own input apart)."""
+    if torch.cuda.is_available():
+        pytest.skip("fake addresses: CPU only")
+    rng = np.random.default_rng(5)
+    D, seen = 2, {1: 0, 3: 0}
+    for trial in range(4000):
+        B, T = int(rng.integers(1, 4)), int(rng.integers(1, 5))
+        f32 = int(rng.integers(0, 2))
+        a = _args(samples=B, rows_per_sample=T, D=D, x_f32=f32, out_f32=int(rng.integers(0, 2)), rope__dim=2, rope__axes=1,
+                  rope__axis_pairs=(1, 0, 0, 0), rope__pt=1)
+        nested = [int(i) for i in rng.permutation(3)]
+        tensors = []
+        for n, t in enumerate((a.q, a.k)):
+            t.heads = int(rng.integers(1, 4))
+            counts = [B, T, t.heads]
+            for x, out in ((True, False), (False, True)):
+                strides, unit = [0, 0, 0], D * int(rng.integers(1, 3))
+                for i in nested:
+                    strides[i] = unit
+                    unit *= counts[i]
+                if rng.random() < 0.5:
+                    strides = [int(rng.integers(0, 3 * D * max(counts))) for _ in range(3)]
+                size = 4 if (a.x_f32 if x else a.out_f32) else 2
+                at = BASE + size * int(rng.integers(0, 60))
+                if x:
+                    t.x, (t.sb, t.st, t.sh) = at, strides
+                else:
+                    if rng.random() < 0.3:
+                        at, strides = t.x, [t.sb, t.st, t.sh]
+                    t.out, (t.ob, t.ot, t.oh) = at, strides
+                tensors.append((n, out, at, strides, counts, size))
+        places = [(n, out, *_bytes(at, [(s * size, c) for s, c in zip(st, counts)], D * size),
+                   (at, size, tuple(s for s, c in zip(st, counts) if c > 1))) for n, out, at, st, counts, size in tensors]
+        if any(p[2][0] % (4 if a.out_f32 else 2) for p in places if p[1]):
+            continue
+        refuse = any(out and len(np.unique(b)) != len(b) for _, out, _, b, _ in places)
+        for i, (n, out, _, b, view) in enumerate(places):
+            for j, (m, other_out, _, c, other) in enumerate(places):
+                if out and i != j and not (n == m and not other_out and view == other):
+                    refuse |= len(np.intersect1d(b, c)) > 0
+        got = L.svdq_rotary(ctypes.byref(a), None)
+        assert got == (1 if refuse else 3), (trial, L.svdq_last_error(), tensors)
+        seen[got] += 1
+    assert min(seen.values()) > 200, seen
