@@ -19,17 +19,43 @@ constexpr long long kMaxStride = 1ll << 38;
 
 bool at16(const void* p) { return aligned16(p); }
 
+// Bytes of a head in a cache.
+int code_bytes(int D, int format) { return format == SVDQ_KV_MXFP4 ? D / 2 : D; }
+int scale_bytes(int D, int format) { return format == SVDQ_KV_MXFP4 ? (D + 31) / 32 : 1; }
+
 // The bytes of a strided tensor: runs of `width` bytes at base + sum of i_d stride_d, 0 <= i_d < n_d (strides in bytes,
 // not negative).
 struct Grid {
-  uintptr_t base;
-  long long width;
-  struct {
+  struct Dim {
     long long stride, n;
-  } dim[3];
-  Grid(const void* p, long long esize, long long run, long long s0 = 0, long long n0 = 1, long long s1 = 0, long long n1 = 1,
-       long long s2 = 0, long long n2 = 1)
-      : base(reinterpret_cast<uintptr_t>(p)), width(run * esize), dim{{s0 * esize, n0}, {s1 * esize, n1}, {s2 * esize, n2}} {}
+  };
+  uintptr_t base, end;  // [base, end) holds all of them (end at most the largest address)
+  long long width;
+  int dims;             // those of more than one index
+  Dim dim[3];
+  Grid() {}
+  Grid(const void* p, long long bytes) : base(reinterpret_cast<uintptr_t>(p)), end(base + bytes), width(bytes), dims(0) {}
+  Grid(const void* p, long long esize, long long run, Dim a, Dim b = {0, 1}, Dim c = {0, 1}) : Grid(p, esize * run) {
+    unsigned __int128 last = end;
+    for (const Dim& d : {a, b, c})
+      if (d.n > 1) {
+        dim[dims++] = {d.stride * esize, d.n};
+        last += static_cast<unsigned __int128>(d.n - 1) * (d.stride * esize);
+      }
+    end = last > UINTPTR_MAX ? UINTPTR_MAX : static_cast<uintptr_t>(last);
+  }
+  // Each dimension steps over all that those of smaller strides span: no two places share a byte.
+  bool nested() const {
+    Dim d[3];
+    std::copy(dim, dim + dims, d);
+    std::sort(d, d + dims, [](const Dim& l, const Dim& r) { return l.stride < r.stride; });
+    __int128 extent = width;
+    for (int i = 0; i < dims; ++i) {
+      if (d[i].stride < extent) return false;
+      extent += static_cast<__int128>(d[i].n - 1) * d[i].stride;
+    }
+    return true;
+  }
 };
 
 // Whether two grids share a byte: whether integers k_u, one for each different stride u, make base' - base + sum of k_u u lie
@@ -39,7 +65,6 @@ struct Grid {
 class Overlap {
  public:
   bool shared(const Grid& a, const Grid& b) {
-    if (reach(a) <= b.base || reach(b) <= a.base) return false;
     add(a, -1);
     add(b, 1);
     before_ = a.width, after_ = b.width;
@@ -47,11 +72,11 @@ class Overlap {
   }
   // whether two places of one grid do
   bool itself(const Grid& g) {
-    for (const auto& d : g.dim)
-      if (d.n > 1 && d.stride < g.width) return true;
-    for (int i = 0; i < 3; ++i)
+    for (int i = 0; i < g.dims; ++i) {
+      if (g.dim[i].stride < g.width) return true;
       for (int j = 0; j < i; ++j)
-        if (g.dim[i].n > 1 && g.dim[j].n > 1 && g.dim[i].stride == g.dim[j].stride) return true;
+        if (g.dim[i].stride == g.dim[j].stride) return true;
+    }
     add(g, -1);
     add(g, 1);
     before_ = after_ = g.width;
@@ -70,14 +95,10 @@ class Overlap {
   long long before_, after_;
   bool different_ = false;  // at least one k is not 0
 
-  static wide reach(const Grid& g) {
-    wide end = static_cast<wide>(g.base) + g.width;
-    for (const auto& d : g.dim) end += static_cast<wide>(d.n - 1) * d.stride;
-    return end;
-  }
   void add(const Grid& g, int sign) {
-    for (const auto& d : g.dim) {
-      if (d.n <= 1 || d.stride == 0) continue;
+    for (int at = 0; at < g.dims; ++at) {
+      const Grid::Dim& d = g.dim[at];
+      if (d.stride == 0) continue;
       int i = 0;
       while (i < terms_ && term_[i].stride > d.stride) ++i;
       if (i == terms_ || term_[i].stride != d.stride) {
@@ -108,7 +129,7 @@ class Overlap {
     return false;
   }
 };
-bool meet(const Grid& a, const Grid& b) { return Overlap().shared(a, b); }
+bool meet(const Grid& a, const Grid& b) { return a.base < b.end && b.base < a.end && Overlap().shared(a, b); }
 
 svdq_status check_norm(const svdq_norm& n, const char* what, int D) {
   if (n.kind < SVDQ_NORM_NONE || n.kind > SVDQ_NORM_LAYER || (n.f32 != 0 && n.f32 != 1) ||
@@ -169,32 +190,59 @@ svdq_status check_sizes(const svdq_heads_args& a) {
   return SVDQ_OK;
 }
 
-Grid input_of(const svdq_heads& h, const svdq_heads_args& a) {
-  return Grid(h.x, a.x_f32 ? 4 : 2, a.D, h.sb, a.samples, h.st, a.rows_per_sample, h.sh, h.heads);
-}
-Grid output_of(const svdq_heads& h, const svdq_heads_args& a) {
-  return Grid(h.out, a.out_f32 ? 4 : 2, a.D, h.ob, a.samples, h.ot, a.rows_per_sample, h.oh, h.heads);
-}
 bool same_view(const Grid& a, const Grid& b) {
-  if (a.base != b.base || a.width != b.width) return false;
-  for (int i = 0; i < 3; ++i)
-    if (a.dim[i].n != b.dim[i].n || (a.dim[i].n > 1 && a.dim[i].stride != b.dim[i].stride)) return false;
-  return true;
+  return a.base == b.base && a.width == b.width && a.dims == b.dims &&
+         std::equal(a.dim, a.dim + a.dims, b.dim, [](const auto& l, const auto& r) { return l.stride == r.stride && l.n == r.n; });
 }
 
-// An output may be its own input (the same view, of one type); else it shares no byte with an input or another output.
-svdq_status check_overlap(const svdq_heads_args& a, const svdq_heads* const* in, int n_in, const svdq_heads* const* out,
-                          int n_out) {
-  for (int o = 0; o < n_out; ++o) {
-    const Grid y = output_of(*out[o], a);
-    if (Overlap().itself(y)) return fail(SVDQ_ERR_INVALID_ARG, "an output's heads overlap");
-    for (int i = 0; i < n_in; ++i) {
-      const Grid x = input_of(*in[i], a);
-      if (!(in[i] == out[o] && same_view(x, y)) && meet(y, x))
-        return fail(SVDQ_ERR_INVALID_ARG, "an output overlaps an input");
+// What a call reads, or what it writes.
+struct Touched {
+  Grid at;
+  const char* name;
+  const svdq_heads* of;  // whose heads: an output of heads may be their own input
+};
+struct TouchedList {
+  Touched item[16];
+  int n = 0;
+  void add(const Grid& g, const char* name, const svdq_heads* of = nullptr) { item[n++] = {g, name, of}; }
+  // a tensor's heads and the vectors of their norm
+  void add_input(const svdq_heads& h, const char* name, const svdq_heads_args& a) {
+    add(Grid(h.x, a.x_f32 ? 4 : 2, a.D, {h.sb, a.samples}, {h.st, a.rows_per_sample}, {h.sh, h.heads}), name, &h);
+    if (h.norm.kind == SVDQ_NORM_NONE) return;
+    if (h.norm.weight != nullptr) add(Grid(h.norm.weight, (h.norm.f32 ? 4 : 2) * a.D), "a norm's weight");
+    if (h.norm.bias != nullptr) add(Grid(h.norm.bias, (h.norm.f32 ? 4 : 2) * a.D), "a norm's bias");
+  }
+  void add_output(const svdq_heads& h, const char* name, const svdq_heads_args& a) {
+    add(Grid(h.out, a.out_f32 ? 4 : 2, a.D, {h.ob, a.samples}, {h.ot, a.rows_per_sample}, {h.oh, h.heads}), name, &h);
+  }
+  void add_rope(const svdq_rope& r, const svdq_heads_args& a) {
+    if (r.dim == 0) return;
+    add(Grid(r.turns, 4 * r.dim), "the turns");
+    add(Grid(r.positions, r.positions_i64 ? 8 : 4, r.axes, {r.pb, a.samples}, {r.pt, a.rows_per_sample}), "the positions");
+  }
+  void add_cache(const svdq_kv_cache& c) {
+    const long long heads = static_cast<long long>(c.pages) * c.page_size * c.heads;
+    for (int i = 0; i < 2; ++i) {
+      add(Grid(c.codes[i], heads * code_bytes(c.D, c.format)), "the cache's codes");
+      add(Grid(c.scales[i], heads * scale_bytes(c.D, c.format)), "the cache's scales");
+    }
+  }
+};
+
+// Every output shares no byte with another place of its own, with what the call reads or with another output, but an output
+// of heads may be their input (the same view, of one type).
+svdq_status check_overlap(const TouchedList& out, const TouchedList& in) {
+  for (int o = 0; o < out.n; ++o) {
+    const Touched& y = out.item[o];
+    if (!y.at.nested() && Overlap().itself(y.at)) return fail(SVDQ_ERR_INVALID_ARG, "%s: places of the output overlap", y.name);
+    for (int i = 0; i < in.n; ++i) {
+      const Touched& x = in.item[i];
+      if (!(x.of != nullptr && x.of == y.of && same_view(x.at, y.at)) && meet(y.at, x.at))
+        return fail(SVDQ_ERR_INVALID_ARG, "%s: the output overlaps %s", y.name, x.name);
     }
     for (int p = 0; p < o; ++p)
-      if (meet(y, output_of(*out[p], a))) return fail(SVDQ_ERR_INVALID_ARG, "outputs overlap");
+      if (meet(y.at, out.item[p].at))
+        return fail(SVDQ_ERR_INVALID_ARG, "%s: the output overlaps %s", y.name, out.item[p].name);
   }
   return SVDQ_OK;
 }
@@ -213,8 +261,6 @@ svdq_status check_cache(const svdq_kv_cache& c) {
   return SVDQ_OK;
 }
 
-int code_bytes(int D, int format) { return format == SVDQ_KV_MXFP4 ? D / 2 : D; }
-int scale_bytes(int D, int format) { return format == SVDQ_KV_MXFP4 ? (D + 31) / 32 : 1; }
 unsigned magic(int d) { return d == 1 ? 0u : static_cast<unsigned>((0x100000000ull + d - 1) / d); }
 
 svdq::heads::Cache device_cache(const svdq_kv_cache& c) {
@@ -381,8 +427,12 @@ svdq_status svdq_rotary(const svdq_heads_args* a, svdq_stream_t stream) {
   if (svdq_status s = check_heads(a->q, "q", *a, true); s != SVDQ_OK) return s;
   if (two)
     if (svdq_status s = check_heads(a->k, "k", *a, true); s != SVDQ_OK) return s;
-  const svdq_heads* const t[2] = {&a->q, &a->k};
-  if (svdq_status s = check_overlap(*a, t, two ? 2 : 1, t, two ? 2 : 1); s != SVDQ_OK) return s;
+  TouchedList in, out;
+  in.add_input(a->q, "q", *a);
+  out.add_output(a->q, "q", *a);
+  if (two) in.add_input(a->k, "k", *a), out.add_output(a->k, "k", *a);
+  in.add_rope(a->rope, *a);
+  if (svdq_status s = check_overlap(out, in); s != SVDQ_OK) return s;
   svdq::heads::Args k{};
   add_part(k, a->q, true);
   if (two) add_part(k, a->k, true);
@@ -421,9 +471,14 @@ svdq_status svdq_kv_write(const svdq_kv_cache* c, const svdq_heads_args* a, cons
   if (svdq_status s = check_heads(a->v, "v", *a, false); s != SVDQ_OK) return s;
   if (a->k.heads != c->heads || a->v.heads != c->heads)
     return fail(SVDQ_ERR_INVALID_ARG, "k of %d heads, v of %d, for a cache of %d", a->k.heads, a->v.heads, c->heads);
-  const svdq_heads* const in[3] = {&a->k, &a->v, &a->q};
-  const svdq_heads* const out[1] = {&a->q};
-  if (svdq_status s = check_overlap(*a, in, q ? 3 : 2, out, q ? 1 : 0); s != SVDQ_OK) return s;
+  TouchedList in, out;
+  if (q) in.add_input(a->q, "q", *a), out.add_output(a->q, "q", *a);
+  in.add_input(a->k, "k", *a);
+  in.add_input(a->v, "v", *a);
+  in.add_rope(a->rope, *a);
+  in.add(Grid(slots, (slots_i64 ? 8ll : 4ll) * a->samples * a->rows_per_sample), "the slots");
+  out.add_cache(*c);
+  if (svdq_status s = check_overlap(out, in); s != SVDQ_OK) return s;
   svdq::heads::Args k{};
   k.cache = device_cache(*c);
   k.slots = slots;
@@ -467,17 +522,23 @@ svdq_status svdq_kv_read(const svdq_kv_cache* c, const int32_t* table, long long
   if (k_row < 0 || k_head < 0 || v_row < 0 || v_head < 0 || k_row >= kMaxStride || k_head >= kMaxStride ||
       v_row >= kMaxStride || v_head >= kMaxStride)
     return fail(SVDQ_ERR_INVALID_ARG, "an output stride is negative or above 2^38");
-  const svdq_heads* const out[2] = {&o.k, &o.v};
-  if (svdq_status s = check_overlap(o, nullptr, 0, out, 2); s != SVDQ_OK) return s;
+  TouchedList in, out;
+  out.add_output(o.k, "keys", o);
+  out.add_output(o.v, "values", o);
+  in.add_cache(*c);
+  in.add(Grid(offsets, 4 * (samples + 1ll)), "the offsets");
+  if (width > 0) in.add(Grid(table, 4, width, {ld_table, samples}), "the table");
+  if (svdq_status s = check_overlap(out, in); s != SVDQ_OK) return s;
   int dev, sms;
   if (svdq_status s = device_ready(&dev, &sms); s != SVDQ_OK) return s;
   svdq::heads::ReadArgs r{};
   for (int i = 0; i < 2; ++i) {
     r.codes[i] = static_cast<const uint8_t*>(c->codes[i]);
     r.scales[i] = static_cast<const uint8_t*>(c->scales[i]);
-    r.out[i] = out[i]->out;
-    r.ot[i] = out[i]->ot;
-    r.oh[i] = out[i]->oh;
+    const svdq_heads& h = i ? o.v : o.k;
+    r.out[i] = h.out;
+    r.ot[i] = h.ot;
+    r.oh[i] = h.oh;
   }
   r.cache = device_cache(*c);
   r.table = table;

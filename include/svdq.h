@@ -540,8 +540,9 @@ typedef struct svdq_heads_args {
   svdq_rope rope;
 } svdq_heads_args;
 
-/* Norm and rotation of q and, unless its heads are 0, of k. `out` may be x itself (the same view, of one type); other
- * overlaps of outputs with anything are refused, unless tensors only lie in different columns of the same rows. D is
+/* Norm and rotation of q and, unless its heads are 0, of k. `out` may be x itself (the same view, of one type); an output
+ * that shares a byte with anything else the call reads or writes, or with another place of its own, is refused, here as in
+ * svdq_kv_write (the cache's planes are outputs there) and svdq_kv_read. Tensors may lie between each other's rows. D is
  * even, at most 256, at most 4096 heads; any strides and element alignment (D and dim multiples of 8 on 16 bytes with
  * strides in multiples of 8 are fast, others are taken value by value). */
 SVDQ_API svdq_status svdq_rotary(const svdq_heads_args* a, svdq_stream_t stream);

@@ -323,3 +323,65 @@ def test_overlaps_are_those_of_the_bytes(L):
         assert got == (1 if refuse else 3), (trial, L.svdq_last_error(), tensors)
         seen[got] += 1
     assert min(seen.values()) > 200, seen
+
+
+NORMED = dict(q__norm__kind=2, q__norm__eps=1e-6, q__norm__f32=1, k__norm__kind=1, k__norm__eps=1e-6)
+OUT = BASE + (1 << 24)  # q's output: 5 rows of 6 heads of 40 bf16 values, 2400 bytes
+
+
+@pytest.mark.parametrize("changes", [
+    dict(rope__positions=OUT), dict(rope__positions=OUT + 2396), dict(rope__positions=OUT - 36), dict(rope__turns=OUT - 56),
+    dict(rope__turns=OUT + 2392), dict(NORMED, q__norm__weight=OUT + 2396), dict(NORMED, q__norm__bias=OUT - 156),
+    dict(NORMED, k__norm__weight=OUT + 2398)])
+def test_outputs_over_what_is_read_are_refused(L, changes):
+    """Positions, frequencies and the norms' vectors whose first or last element lies in q's output."""
+    assert L.svdq_rotary(ctypes.byref(_args(**changes)), None) == 1
+    assert b"overlaps" in L.svdq_last_error()
+    assert _write(L, **changes) == 1 and b"overlaps" in L.svdq_last_error()
+
+
+@pytest.mark.parametrize("changes", [
+    dict(rope__positions=OUT + 2400), dict(rope__positions=OUT - 40), dict(rope__turns=OUT - 64), dict(rope__turns=OUT + 2400),
+    dict(NORMED, q__norm__weight=OUT + 2400), dict(NORMED, q__norm__bias=OUT - 160), dict(NORMED, k__norm__weight=OUT - 80),
+    dict(q__norm__weight=OUT),                                        # no norm: its vectors are not read
+    dict(q__ot=480, rope__positions=OUT + 480, rope__pt=240)])        # positions behind each row's heads
+def test_outputs_beside_what_is_read_are_taken(L, changes):
+    if torch.cuda.is_available():
+        pytest.skip("fake addresses: CPU only")
+    assert L.svdq_rotary(ctypes.byref(_args(**changes)), None) == 3, L.svdq_last_error()
+    assert _write(L, **changes) == 3, L.svdq_last_error()
+
+
+CODES, SCALES = 7 * 16 * 2 * 40, 7 * 16 * 2  # bytes of a plane
+
+
+def test_a_cache_over_what_the_write_touches_is_refused(L):
+    k0, s1 = BASE + (30 << 24), BASE + (33 << 24) + 1
+    for changes in (dict(k__x=k0 + CODES - 2), dict(v__x=k0), dict(q__out=k0 + CODES - 2), dict(q__x=k0), dict(v__x=s1 + SCALES - 1),
+                    dict(rope__positions=k0 + 4)):
+        assert _write(L, **changes) == 1 and b"overlaps" in L.svdq_last_error(), changes
+    assert _write(L, slots=ctypes.c_void_p(k0 + CODES - 4)) == 1 and b"the slots" in L.svdq_last_error()
+    assert _write(L, slots=ctypes.c_void_p(k0 - 32), i64=1) == 1 and b"the slots" in L.svdq_last_error()
+    for field, i, at in (("codes", 1, k0), ("codes", 1, k0 + CODES - 16), ("scales", 0, k0 + 5), ("scales", 1, BASE + (32 << 24) + SCALES)):
+        c = _cache()
+        getattr(c, field)[i] = at
+        assert _write(L, c) == 1 and b"the cache's" in L.svdq_last_error(), (field, i)
+    if not torch.cuda.is_available():
+        c = _cache()
+        c.codes[1], c.scales[0], c.scales[1] = k0 + CODES, k0 + 2 * CODES, k0 + 2 * CODES + SCALES   # one buffer, no gaps
+        assert _write(L, c, v__x=k0 - 800, q__out=k0 + 2 * CODES + 2 * SCALES) == 3, L.svdq_last_error()
+
+
+def test_values_over_what_the_read_touches_are_refused(L):
+    """9 rows of 2 heads of 40 (1440 bytes) over the cache's planes, the table and the offsets."""
+    at = lambda b: (b - BASE) / 2 ** 24
+    k0, s1 = BASE + (30 << 24), BASE + (33 << 24) + 1
+    for changes in (dict(k=at(k0 - 1438)), dict(v=at(k0 + CODES - 2)), dict(k=at(s1 + SCALES - 1)), dict(v=at(SLOTS.value + 44)),
+                    dict(k=at(SLOTS.value - 1438))):
+        assert _read(L, **changes) == 1 and b"overlaps" in L.svdq_last_error(), changes
+    far = ctypes.c_void_p(BASE + (60 << 24))
+    assert _read(L, offsets=far, k=60 + 12 / 2 ** 24) == 1 and b"the offsets" in L.svdq_last_error()
+    if not torch.cuda.is_available():
+        assert _read(L, k=at(k0 - 1440), v=at(k0 + CODES), offsets=far) == 3, L.svdq_last_error()
+        assert _read(L, offsets=far, k=60 + 16 / 2 ** 24) == 3, L.svdq_last_error()
+        assert _read(L, table=SLOTS, offsets=far, width=0, ld=0, k=40) == 3, L.svdq_last_error()
