@@ -52,15 +52,29 @@ def includes(path: str) -> set[str]:
 DEPS = sorted(set().union(*(includes(s) for s in SOURCES)))
 
 
-def _newer(target: str, deps) -> bool:
-    if not os.path.exists(target):
+def _current(target: str, deps, flags) -> bool:
+    """Whether a file is newer than all it was made from and was made with these flags (recorded beside it)."""
+    if not os.path.exists(target) or not os.path.exists(target + ".flags"):
         return False
+    with open(target + ".flags") as f:
+        if f.read() != "\n".join(flags):
+            return False
     t = os.path.getmtime(target)
     return all(os.path.getmtime(d) <= t for d in deps)
 
 
-def up_to_date() -> bool:
-    return _newer(LIB_PATH, DEPS)
+def _make(target: str, flags, cmd, verbose):
+    """Runs the command that writes target + ".tmp"; the file is then replaced, with the record of its flags."""
+    _run(cmd, verbose)
+    if os.path.exists(target + ".flags"):
+        os.remove(target + ".flags")
+    os.replace(target + ".tmp", target)
+    with open(target + ".flags", "w") as f:
+        f.write("\n".join(flags))
+
+
+def up_to_date(extra=None) -> bool:
+    return _current(LIB_PATH, DEPS, [*NVCC_FLAGS, *(extra or [])])
 
 
 def _run(cmd, verbose):
@@ -75,23 +89,21 @@ def _run(cmd, verbose):
 
 def build(force: bool = False, verbose: bool = False, extra=None) -> str:
     """One object per source, compiled side by side (an object that is newer than all its source includes
-    is kept), linked into the library."""
-    if not force and up_to_date():
+    and has the same flags is kept), linked into the library."""
+    if not force and up_to_date(extra):
         return LIB_PATH
-    flags = [nvcc(), *NVCC_FLAGS, *(extra or []), "-I", INCLUDE, "-I", CSRC]
+    flags = [*NVCC_FLAGS, *(extra or [])]
+    cmd = [nvcc(), *flags, "-I", INCLUDE, "-I", CSRC]
 
     def compile_one(src):
         obj = src[:-3] + ".o"
-        if force or not _newer(obj, includes(src)):
-            _run([*flags, "-c", "-o", obj + ".tmp", src], verbose)
-            os.replace(obj + ".tmp", obj)
+        if force or not _current(obj, includes(src), flags):
+            _make(obj, flags, [*cmd, "-c", "-o", obj + ".tmp", src], verbose)
         return obj
 
     with ThreadPoolExecutor(len(SOURCES)) as pool:
         objects = list(pool.map(compile_one, SOURCES))
-    tmp = LIB_PATH + ".tmp"
-    _run([*flags, "-shared", "-o", tmp, *objects], verbose)
-    os.replace(tmp, LIB_PATH)
+    _make(LIB_PATH, flags, [*cmd, "-shared", "-o", LIB_PATH + ".tmp", *objects], verbose)
     return LIB_PATH
 
 
