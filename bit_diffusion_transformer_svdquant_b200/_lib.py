@@ -1062,7 +1062,8 @@ def mlp_mx(x, w_up: MxWeight, w_down: MxWeight, bias_up=None, bias_down=None, no
 
 # ---------------------------------------------------------------- rotary positions, key/value cache
 
-# 2 pi to 2^-190: a double's would be off by 10^-7 rad at a position of 2^31
+# 2 pi to 2^-190. Frequencies are doubles; those that are exact, such as every axis's first (1 rad per position without
+# scaling), would be off by 10^-7 rad at a position of 2^31 with a double's 2 pi. Others are off by as much themselves.
 _TWO_PI = Fraction(628318530717958647692528676655900576839433879875021164194989, 10 ** 59)
 
 
@@ -1074,8 +1075,8 @@ class Rotary:
         {"kind": "linear", "factor": s}     f / s
         {"kind": "ntk", "factor": s}        theta s^(d / (d - 2)) in place of theta
         {"kind": "yarn", "factor": s, "length": L, "beta_fast": 32, "beta_slow": 1, "amplitude": None}
-            f (g + (1 - g) / s) with g = (L f / 2 pi - slow) / (fast - slow) within [0, 1]: pairs that turn more than
-            `fast` times over the trained length L keep their frequency, those below `slow` are stretched; the
+            f (g + (1 - g) / s) with g = (L f / 2 pi - slow) / (fast - slow) within [0, 1], a ramp over the pair's turns
+            (not over pair indices rounded at its ends, as some models' code has it): pairs that turn more than `fast` times over the trained length L keep their frequency, those below `slow` are stretched; the
             rotated values are multiplied by `amplitude` (None: 0.1 ln s + 1)."""
 
     def __init__(self, dim: int, axes=None, layout: str = "interleaved", theta: float = 10000.0,

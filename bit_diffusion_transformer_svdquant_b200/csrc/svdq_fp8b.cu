@@ -246,7 +246,9 @@ svdq_status check_gemm(const svdq_fp8b_act* act, const svdq_fp8b_weight* w, cons
 
 // Where the few-row kernels run (measured on B200 with weights from HBM, us of the few-row kernel / the other).
 // The quantizer with a branch up to 384 rows: K = 3072, r = 32: 4.2 / 11.8 at one row, 9.5 / 11.7 at 384, 15.7 / 11.7 at
-// 512; K = 12288: 8.1 / 27.8, 25.0 / 27.8, 42.2 / 28.0; K = 256: 3.1 / 5.2, 5.5 / 5.4, 8.6 / 5.4.
+// 512; K = 12288: 8.1 / 27.8, 25.0 / 27.8, 42.2 / 28.0; K = 256: 3.1 / 5.2, 5.5 / 5.4, 8.6 / 5.4. The few-row one sums U on the
+// CUDA cores, every row its own: at 384 x 12288 instructions bound it (issue 60 %, ALU 44 %, DRAM 4 %). Kernel 1 takes as long
+// for 1 row as for 512: at most 4 CTAs go through the K of 128 rows.
 bool few_quant_rows(int M, int K_pad) { return M <= 384 && K_pad <= svdq::mx::kFewQuantMaxK - 1024; }
 struct FewSplit {
   int blocks, ranks;  // CTA clusters over N, and their size over K

@@ -15,7 +15,8 @@
 //
 // The layer keeps its structure (smoothing, 16-bit low-rank branch, quantized residual): kernel 1 is
 // svdq::quant_act_kernel with the Act policy below, the product svdq::pair_gemm_kernel with the Gemm policy.
-// Rows and columns of padding hold zero codes, so that sizes need not fill a tile.
+// Columns past K and the weight's rows past N hold zero codes, so that sizes need not fill a tile. Activation rows past M
+// are not written: what they hold reaches only their own outputs, which are not stored.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -87,9 +88,10 @@ struct ActArgs {
 };
 
 // The quantizer policy of quant_act_kernel: a block spans two 64-wide stages, so a group of quantizer warps takes
-// two at a time; a thread owns 16 columns of both stages in two rows, the four lanes of a row its block. Reading X
-// bounds it where row tiles fill the SMs: on B200 4608 rows of 3072, r = 32, 13.6 us (3.1 TB/s of X, codes and scales); below
-// that latency: 512 rows 11.5 us, of K = 1608, r = 16, 8.4 us with K in shares of 4, 4, 4 and 1 blocks (15.4 us unsplit).
+// two at a time; a thread owns 16 columns of both stages in two rows, the four lanes of a row its block. Latency
+// bounds it: on B200 4608 rows of 3072, r = 32, 13.9 us (3.1 TB/s of X, codes and scales, 0.47 of the copy rate), where clusters
+// of three put 108 of 148 SMs to work, each goes through 16 stages once and no unit is half full (issue 35 %, ALU 33 %);
+// 512 rows 11.5 us, of K = 1608, r = 16, 8.4 us with K in shares of 4, 4, 4 and 1 blocks (15.4 us unsplit).
 struct Act {
   using Args = ActArgs;
   static constexpr int kRun = 2;
@@ -284,8 +286,8 @@ struct GemmArgs {
 // The block-scaled FP8 format of the pair GEMM. A K step is one block of 128: its four MMAs (K = 32) take the same
 // scale byte, byte kt % 4 of the atom that four K steps share. The writers then hand a scale buffer over once per four
 // steps; with an atom in every ring slot and a hand-over per step (512 tensor-pipe cycles), 4608 x 3072 x 9216 took 117 us on
-// B200 instead of 97. What an SM takes in bounds it: some 45 bytes a cycle, with 18 SMs at work as with all. Hence tiles
-// 384 wide (53 bytes of codes per tensor-pipe cycle, 64 at 256 wide, 96 at 128), issued as N = 256 and N = 128 on the
+// B200 instead of 97. An SM took in 44 to 51 bytes a cycle at every size and tile measured, with 18 SMs at work as with
+// all. Hence tiles 384 wide (53 bytes of codes per tensor-pipe cycle, 64 at 256 wide, 96 at 128), issued as N = 256 and N = 128 on the
 // same A; 256 wide the next took 354 us. Between tiles its one accumulator waits: 256 columns twice leave TMEM no room
 // for scales. 16896 x 3072 x 9216 340 us, 4608 x 3072 x 24576 with SwiGLU (256 wide), bias and r = 32 277 us (2.8 and 2.5
 // PFLOP/s). Scales read by their writers from global memory instead of bulk copies: 349 us (and 5 % less at few rows).

@@ -384,8 +384,11 @@ svdq_status run_heads(const svdq_heads_args& a, svdq::heads::Args& k, svdq_strea
       if (round_up(units, w) < round_up(units, block)) block = w;
     if (units < block) block = units;
     const int columns = (units + block - 1) / block;
-    // Rows per block: all blocks on the SMs at once (32 warps an SM, by registers), so that their start and end are paid
-    // once; where some parts cost more than others (rotation, norm) three rounds of blocks even that out, if strips stay
+    // Rows per block: as many blocks as make 32 warps an SM, which registers allow, so that their start and end are paid
+    // once. (Blocks of one or two warps, of one to four heads, do not all fit: their tables let 11 blocks on an SM, and the
+    // grid takes 1.5 to 3 rounds. With 11 blocks counted in their place, us here / there: 4608 rows of 1 head 7.3 / 4.6, of 4
+    // 7.1 / 5.2; 16896 rows of 1 12.0 / 11.8, of 4 12.8 / 14.8; 65536 rows of 1 34.5 / 36.6, of 4 43.4 / 40.4: better for some,
+    // worse for others, as strips are whole batches.) Where some parts cost more than others (rotation, norm) three rounds of blocks even that out, if strips stay
     // long (16384 tokens written, 72 heads of 128: 115, 110, 104 and 105 us at 1 to 4 rounds; q and k of 16896 rows, all
     // alike: 70, 73, 75 us at 1 to 3).
     const long long columns_all = static_cast<long long>(columns) * k.samples;

@@ -4,8 +4,9 @@
 // Rotation of the first `dim` values of a head, pair p of dim / 2 on axis a(p), by the angle pos[a] f_p:
 //   o0 = A (x0 cos - x1 sin),  o1 = A (x1 cos + x0 sin)
 // on (x[2p], x[2p + 1]) (interleaved) or (x[p], x[p + dim/2]) (half). The frequency comes as turns per position
-// in 64-bit fixed point, F = round(f / 2 pi 2^64): the low 64 bits of pos F are the turns modulo one, so that an angle is
-// exact to pos 2^-65 turns whatever the position (in fp32, pos f is off by 0.03 rad at a position of 10^6).
+// in 64-bit fixed point, F = round(f / 2 pi 2^64): the low 64 bits of pos F are the turns modulo one, off by |pos| 2^-65 at
+// most, of which the kernel keeps the upper 32 (in fp32, pos f is off by 0.03 rad at a position of 10^6). So an angle
+// is that of f to |pos| 2^-65 + 2^-32 turns; the first term passes the second beyond |pos| = 2^33.
 //
 // Everything between a load and its store is fp32; norm statistics too.
 #pragma once
@@ -193,10 +194,12 @@ struct Raw<float, HALF> {
 // strip of rows (blockIdx.x) of one sample (blockIdx.z). So a lane's columns, weights and strides are fixed and a row
 // costs it a load, a store and the arithmetic; kAhead rows of loads are in flight. The cosines and sines of kBatch
 // rows are computed by the whole block at a time, into one half of a table while the heads read the other.
-// Measured on B200: q and k of 16896 rows of 24 heads of 128 with norms 69.6 us (6.0 TB/s, 0.91 of the copy rate), without
-// 19.0 us for 4608 rows (6.0 TB/s); 16384 tokens written in FP8 with q 103 us (4.9 TB/s); one token 3.0 us. What bounds it
-// is instruction issue (63 % in the write) together with the latency that 32 warps an SM leave uncovered. With a warp per row
-// and its heads in turn (coefficients in registers, pointers per head) the first took 83 us.
+// Measured on B200: q and k of 16896 rows of 24 heads of 128 with norms 69.7 us (6.0 TB/s, 0.91 of the copy rate), 4608 rows
+// 22.5 us, without norms 21.3; 16384 tokens written in FP8 with q 103 us (4.9 TB/s); one token 3.0 us. What bounds it is the
+// latency that 32 warps an SM leave uncovered (of 13 warps per issue 5.3 wait for memory in the first) together with
+// instruction issue (56 %; in the write 63 %). With a warp per row and its heads in turn (coefficients in registers,
+// pointers per head) the first took 83 us. Heads of other sizes, 16896 rows of as many bytes: 64 70.6 us; 256 81.9, 96 89.0,
+// 80 103, 40 104, 72 117: all in the form with branches, and lanes past D / 8 idle (3 of 8 at 40, 7 of 16 at 72).
 template <class T>
 constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
 constexpr int kBatch = 8;
@@ -506,8 +509,8 @@ __global__ void __launch_bounds__(kThreads, 4) heads_kernel(const __grid_constan
 
 // ---------------------------------------------------------------- any head size, stride and alignment
 // A warp per head; value d is lane d % 32's, and its partner comes through shared memory. Not fast: one head in
-// flight per warp, element by element, angles by each head (4608 rows, q and k of 24 heads of 126: 195 us; of 128 by
-// the kernel above 23 us).
+// flight per warp, element by element, angles by each head (4608 rows, q and k of 24 heads of 126, or of 128 off 16 bytes:
+// 197 us with norms, 151 without; of 128 by the kernel above 22.5 and 21.3).
 template <class T>
 __global__ void __launch_bounds__(kThreads) heads_any_kernel(const __grid_constant__ Args a) {
   constexpr int kPer = kMaxD / 32;

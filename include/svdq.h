@@ -507,8 +507,8 @@ SVDQ_API svdq_status svdq_fp8b_dequantize_act(const svdq_fp8b_act* act, void* ou
  * pos[axis] f_p:
  *   o0 = A (x0 cos - x1 sin),  o1 = A (x1 cos + x0 sin)      (inverse: by the negative angle)
  * on (x[2p], x[2p + 1]), or with `half` on (x[p], x[p + dim/2]); values from dim on stay. turns[p] is the frequency in
- * turns per position, round(f_p / 2 pi 2^64), which makes the angle exact for any 32- or 64-bit integer position (to
- * 2^-32 turns, fp32's own step). With a norm the head is normalised over its D values first (svdq_norm; weight and bias
+ * turns per position, round(f_p / 2 pi 2^64): the angle of any 32- or 64-bit integer position is that of f_p to
+ * |pos| 2^-65 + 2^-32 turns (the first term passes the second beyond |pos| = 2^33). With a norm the head is normalised over its D values first (svdq_norm; weight and bias
  * of D values are shared by the heads). Everything is computed in fp32 and rounded once, when stored. */
 typedef struct svdq_rope {
   int dim;                    /* rotated values, even, <= D; 0: none (svdq_kv_write only)      */
