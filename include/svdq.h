@@ -543,8 +543,9 @@ typedef struct svdq_heads_args {
 /* Norm and rotation of q and, unless its heads are 0, of k. `out` may be x itself (the same view, of one type); an output
  * that shares a byte with anything else the call reads or writes, or with another place of its own, is refused, here as in
  * svdq_kv_write (the cache's planes are outputs there) and svdq_kv_read. Tensors may lie between each other's rows. D is
- * even, at most 256, at most 4096 heads; any strides and element alignment (D and dim multiples of 8 on 16 bytes with
- * strides in multiples of 8 are fast, others are taken value by value). */
+ * even, at most 256, at most 4096 heads; any strides and element alignment. D and dim multiples of 8 on 16 bytes with
+ * strides in multiples of 8 are fast; a call with any other tensor is taken value by value, its norms' sums in another
+ * order, so that results may differ by a rounding. */
 SVDQ_API svdq_status svdq_rotary(const svdq_heads_args* a, svdq_stream_t stream);
 
 /* A paged cache of keys (plane 0) and values (plane 1). Slot s = page * page_size + offset holds a token:
